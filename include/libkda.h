@@ -380,6 +380,118 @@ kda_status_t kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v,
  * counterpart. Allocates nothing. Errors: KDA_ERR_INVALID_ARG (status NULL), KDA_ERR_CUDA. */
 kda_status_t kda_chunk_fwd_noalloc_status(void *stream, int32_t *status);
 
+/* ---- Latent attention: the full-attention layers that stand between the KDA layers -------------
+ * (1 layer in 4: KimiLinear KDA/MLA tutorial (icman.com.cn), sec. 2-3; no position encoding in its
+ * shared part: lpnh.cn article, sec. 3-5.) Every token has one latent vector of 512 channels that
+ * all heads share, and a shared key part of 64 channels (dr = 64) or none (dr = 0). The pages print
+ * no formula; these are softmax attention read plainly.
+ * In addition to the general rules: tensors are bf16 (KDA_F32 returns KDA_ERR_UNSUPPORTED), products
+ * run on the tensor cores with fp32 sums, softmax statistics are fp32, and the probabilities are
+ * rounded to bf16 as the second product's operand. scale must be positive and finite.
+ *
+ * Expanded form, for prompts and training: keys and values per head, expanded from the latent by the
+ * caller's projection.
+ *     s_ij = scale (q_i[:dk] . k_j + q_i[dk:] . k_shared_j),  out_i = sum_j softmax_j(s_ij) v_j
+ *   q          [B, T, H, dk + dr] bf16, dk = 128
+ *   k, v       [B, Tk, H, 128] bf16, with strides in elements between tokens and between heads (they
+ *              may be views of one tensor); channels contiguous, batch rows Tk tokens apart
+ *   k_shared   [B, Tk, dr] bf16 with a token stride, or NULL when dr = 0
+ *   cu_seqlens, cu_seqlens_k  both NULL: N = B, batch row b has T queries and Tk keys. Otherwise int32
+ *              [N+1] device arrays of packed offsets of the queries and of the keys (B = 1): first 0,
+ *              non-decreasing, last T (Tk). A violation writes KDA_ERR_INVALID_ARG to the workspace
+ *              status word; sequences whose offsets lie outside the tensors are skipped.
+ *   causal     nonzero: query i of a sequence with Lq queries and Lk keys sees the keys
+ *              j <= i + Lk - Lq (its last query sees every key: new tokens behind a history).
+ *              Zero: every key of its sequence.
+ *   out        [B, T, H, 128] bf16 (written)
+ *   lse        [B, T, H] float32 (written): log sum_j exp(s_ij)
+ *              A query that sees no key gets out = 0 and lse = -infinity.
+ *   workspace  kda_latent_fwd_workspace_size(...) bytes; its status word is cleared by the call.
+ * Strides are positive multiples of 8; pointers 16-byte aligned (lse, offsets: 4). At most 65535 heads
+ * and 65535 sequences. */
+size_t kda_latent_fwd_workspace_size(int B, int T, int Tk, int H, int N, int dr);
+kda_status_t kda_latent_fwd(const void *q, const void *k, const void *v, const void *k_shared,
+                            const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
+                            void *out, float *lse,
+                            int B, int T, int Tk, int H, int N, int dk, int dv, int dr,
+                            long long k_token_stride, long long k_head_stride,
+                            long long v_token_stride, long long v_head_stride,
+                            long long shared_token_stride, int causal, float scale,
+                            kda_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward pass of kda_latent_fwd: the same arguments, its out and lse, and dout [B, T, H, 128] bf16.
+ * Written, dense and bf16 (summed in fp32, rounded once): dq [B, T, H, dk + dr], dk_out and dv_out
+ * [B, Tk, H, 128], dk_shared [B, Tk, dr] (the sum over the heads; NULL when dr = 0). Results do not
+ * depend on timing: no atomic sums. Workspace: kda_latent_bwd_workspace_size(...) bytes. Keys that no
+ * query sees get zero gradients. */
+size_t kda_latent_bwd_workspace_size(int B, int T, int Tk, int H, int N, int dr);
+kda_status_t kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_shared,
+                            const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,
+                            const void *out, const float *lse, const void *dout,
+                            void *dq, void *dk_out, void *dv_out, void *dk_shared,
+                            int B, int T, int Tk, int H, int N, int dk, int dv, int dr,
+                            long long k_token_stride, long long k_head_stride,
+                            long long v_token_stride, long long v_head_stride,
+                            long long shared_token_stride, int causal, float scale,
+                            kda_dtype_t dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Absorbed form, for decoding over a paged cache: the caller's queries are already multiplied into the
+ * latent space, and the outputs stay in it.
+ *     s_j = scale (q[:dc] . c_j + q[dc:] . r_j),   out = sum_j softmax_j(s_j) c_j
+ *   q          [N, Tq, H, dc + dr] bf16, dc = 512: Tq >= 1 new tokens per sequence
+ *   cache      [num_pages, page_size, dc + dr] bf16: rows [c_j, r_j]; page_size a multiple of 16
+ *   page_table int32 [N, max_pages]: row j of sequence n is row j % page_size of page
+ *              page_table[n][j / page_size]; entries behind a sequence's last page are not read
+ *   seq_lens   int32 [N]: cached rows per sequence, the Tq new ones included (0: an idle slot). New
+ *              token t sees the first seq_len - Tq + t + 1 rows.
+ *   out        [N, Tq, H, dc] bf16, lse [N, Tq, H] float32 (both written); a token that sees no row
+ *              gets out = 0 and lse = -infinity.
+ * Rows behind a sequence's length may hold anything, infinities and NaN included. A length outside
+ * [0, max_pages * page_size] (the sequence is then treated as idle) or a page outside [0, num_pages)
+ * (the sequence's outputs are then not usable; no memory outside the cache is read) writes
+ * KDA_ERR_INVALID_ARG to the status word. num_pages * page_size and max_pages * page_size stay
+ * below 2^31. Workspace: kda_latent_decode_workspace_size(...) bytes (partial results of sequences that
+ * several blocks share), not shared by calls that may overlap. */
+size_t kda_latent_decode_workspace_size(int N, int Tq, int H);
+kda_status_t kda_latent_decode_step(const void *q, const void *cache, const int32_t *page_table,
+                                    const int32_t *seq_lens, void *out, float *lse,
+                                    int N, int Tq, int H, int dc, int dr, int page_size,
+                                    long long num_pages, int max_pages, float scale, kda_dtype_t dtype,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* The cache append in front of it: cache row slots[t] = [norm(c_t), k_shared_t] for T new tokens, with
+ * norm(c) = c / sqrt(mean(c^2) + eps) * weight (weight fp32 [dc]; NULL: c as it is).
+ *   c [T, dc], k_shared [T, dr] (or NULL) bf16 with token strides (positive multiples of 8, or 0);
+ *   slots int64 [T]: row of the cache seen as [cache_rows, dc + dr]. Slots outside [0, cache_rows) are
+ *   skipped (padding); every other slot at most once per call. */
+kda_status_t kda_latent_append(const void *c, const void *k_shared, const long long *slots, const float *weight,
+                               void *cache, long long c_token_stride, long long shared_token_stride,
+                               long long cache_rows, int T, int dc, int dr, float eps, kda_dtype_t dtype,
+                               void *stream);
+
+/* ---- Root-mean-square norm in front of a layer, with the residual's addition ---------------------
+ *     h = x + residual (rounded to dtype; h = x when residual is NULL),
+ *     y = h / sqrt(mean(h^2) + eps) * weight
+ *   x, residual, y, h [rows, D] dtype (fp32 or bf16), weight fp32 [D]. D a multiple of 8, at most 16384
+ *   (else KDA_ERR_UNSUPPORTED). h is written only with a residual, and may alias x or residual; y may
+ *   alias x or residual when the other does not need them. Sums are fp32. 16-byte aligned pointers.
+ * kda_rms_norm_e4m3 writes y in 8 bits (e4m3) instead, with one fp32 scale per 128 channels (D a
+ * multiple of 128): scale [rows, D / 128] = max |y| / 448, y = q * scale. A group of zeros gets scale 0.
+ * A group that holds a NaN or an infinity has a scale that is not finite. */
+kda_status_t kda_rms_norm(const void *x, const void *residual, const float *weight, void *y, void *h,
+                          long long rows, int D, float eps, kda_dtype_t dtype, void *stream);
+kda_status_t kda_rms_norm_e4m3(const void *x, const void *residual, const float *weight, void *y, float *scale,
+                               void *h, long long rows, int D, float eps, kda_dtype_t dtype, void *stream);
+
+/* Its backward pass: dx = the gradient through the norm at h, plus dh (the gradient that reaches h along
+ * the residual stream; NULL: none): the gradient of x and of the residual alike. dweight fp32 [D]
+ * (written; zeros for rows = 0). dy, h, dh, dx [rows, D] dtype; dx may alias dy, h or dh. No atomic sums.
+ * Workspace: kda_rms_norm_bwd_workspace_size(rows, D) bytes, 16-byte aligned (no status word). */
+size_t kda_rms_norm_bwd_workspace_size(long long rows, int D);
+kda_status_t kda_rms_norm_bwd(const void *dy, const void *h, const float *weight, const void *dh, void *dx,
+                              float *dweight, long long rows, int D, float eps, kda_dtype_t dtype,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
 /* Self-test of the library's failure detection (the pages have no counterpart): every device-side
  * wait of the kernels (on an mbarrier or a copy) is bounded and, when it runs out, records
  * KDA_ERR_TIMEOUT in the workspace status word and lets the kernel return, so that the CUDA context

@@ -12,6 +12,9 @@ Names follow the C entry points:
 * ``chunk_prep(q, k, log_alpha, beta, workspace, ...)`` and ``chunk_scan(v, workspace, ...)``:
   the two passes of ``chunk_fwd`` for bf16 inputs, one call each
 * ``chunk_fwd_workspace_size``, ``workspace_status``, ``status_string``
+* the latent attention that stands between KDA layers and the norm in front of a layer (``latent.py``):
+  ``latent_fwd``, ``latent_bwd``, ``latent_decode_step``, ``latent_append``, ``rms_norm``,
+  ``rms_norm_e4m3``, ``rms_norm_bwd``
 """
 from __future__ import annotations
 
@@ -24,6 +27,8 @@ import torch
 __all__ = ["chunk_fwd", "chunk_prep", "chunk_scan", "decode_step", "chunk_fwd_workspace_size", "workspace_status",
            "status_string", "library_path", "load", "KDAError", "cu_seqlens_from_mask", "unpad", "pad",
            "chunk_fwd_noalloc", "noalloc_status",
+           "latent_fwd", "latent_bwd", "latent_decode_step", "latent_append", "latent_bwd_workspace_size",
+           "latent_decode_workspace_size", "rms_norm", "rms_norm_e4m3", "rms_norm_bwd", "rms_norm_bwd_workspace_size",
            "KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_UNSUPPORTED", "KDA_ERR_CUDA", "KDA_ERR_TIMEOUT"]
 
 KDA_OK, KDA_ERR_INVALID_ARG, KDA_ERR_UNSUPPORTED, KDA_ERR_CUDA, KDA_ERR_TIMEOUT = range(5)
@@ -43,7 +48,10 @@ EXPORTS = ("kda_chunk_fwd_workspace_size", "kda_chunk_fwd", "kda_decode_step",
            "kda_workspace_status", "kda_status_string", "kda_version", "kda_chunk_fwd_noalloc",
            "kda_chunk_prep", "kda_chunk_scan", "kda_selftest_wait_timeout",
            "kda_chunk_bwd_workspace_size", "kda_chunk_bwd", "kda_chunk_bwd_phase",
-           "kda_chunk_fwd_noalloc_status", "kda_chunk_fwd_kernel_launches")
+           "kda_chunk_fwd_noalloc_status", "kda_chunk_fwd_kernel_launches",
+           "kda_latent_fwd_workspace_size", "kda_latent_fwd", "kda_latent_bwd_workspace_size", "kda_latent_bwd",
+           "kda_latent_decode_workspace_size", "kda_latent_decode_step", "kda_latent_append",
+           "kda_rms_norm", "kda_rms_norm_e4m3", "kda_rms_norm_bwd_workspace_size", "kda_rms_norm_bwd")
 
 
 class LayerOpts(ctypes.Structure):
@@ -132,6 +140,29 @@ def load():
     lib.kda_short_conv_step.restype = I
     lib.kda_state_affine.argtypes = [P, P, P, P, I, I, I, P]
     lib.kda_state_affine.restype = I
+    L, F = ctypes.c_longlong, ctypes.c_float
+    lib.kda_latent_fwd_workspace_size.argtypes = [I] * 6
+    lib.kda_latent_fwd_workspace_size.restype = Z
+    lib.kda_latent_fwd.argtypes = [P] * 8 + [I] * 8 + [L] * 5 + [I, F, I, P, Z, P]
+    lib.kda_latent_fwd.restype = I
+    lib.kda_latent_bwd_workspace_size.argtypes = [I] * 6
+    lib.kda_latent_bwd_workspace_size.restype = Z
+    lib.kda_latent_bwd.argtypes = [P] * 13 + [I] * 8 + [L] * 5 + [I, F, I, P, Z, P]
+    lib.kda_latent_bwd.restype = I
+    lib.kda_latent_decode_workspace_size.argtypes = [I, I, I]
+    lib.kda_latent_decode_workspace_size.restype = Z
+    lib.kda_latent_decode_step.argtypes = [P] * 6 + [I] * 6 + [L, I, F, I, P, Z, P]
+    lib.kda_latent_decode_step.restype = I
+    lib.kda_latent_append.argtypes = [P] * 5 + [L, L, L, I, I, I, F, I, P]
+    lib.kda_latent_append.restype = I
+    lib.kda_rms_norm.argtypes = [P] * 5 + [L, I, F, I, P]
+    lib.kda_rms_norm.restype = I
+    lib.kda_rms_norm_e4m3.argtypes = [P] * 6 + [L, I, F, I, P]
+    lib.kda_rms_norm_e4m3.restype = I
+    lib.kda_rms_norm_bwd_workspace_size.argtypes = [L, I]
+    lib.kda_rms_norm_bwd_workspace_size.restype = Z
+    lib.kda_rms_norm_bwd.argtypes = [P] * 6 + [L, I, F, I, P, Z, P]
+    lib.kda_rms_norm_bwd.restype = I
     _lib = lib
     return lib
 
@@ -475,3 +506,7 @@ def state_affine(Phi, S_in, Psi=None, out=None):
         raise KDAError(st, "kda_state_affine")
     return out
 
+
+from .latent import (latent_append, latent_bwd, latent_bwd_workspace_size, latent_decode_step,  # noqa: E402
+                     latent_decode_workspace_size, latent_fwd, rms_norm, rms_norm_bwd, rms_norm_bwd_workspace_size,
+                     rms_norm_e4m3)

@@ -16,6 +16,8 @@ constexpr size_t kStatusBytes = 256;  // workspace prefix holding the device sta
 // Lowest cumulative log-decay within one chunk (per channel) that the chunked kernels take: they
 // factor e^{g_r - g_i} = e^{g_r} e^{-g_i}, and e^{-g} must stay finite in fp32.
 constexpr float kMinChunkLogDecay = -80.f;
+constexpr int kLatentDim = 512;       // channels of the latent vector the latent attention shares over heads
+constexpr int kSharedDim = 64;        // channels of its shared key part, where there is one
 constexpr int kMaxGridDim = 65535;    // heads and sequences index grid dimensions y and z of the
                                       // chunked kernels
 

@@ -1,0 +1,75 @@
+// latent.cuh -- what the latent attention's kernels share: the problem's description, the sequences'
+// offsets, and the checks of both.
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+// The expanded form: q [tokens, H, 128 + R] and out [tokens, H, 128] dense; k and v [keys, H, 128] with
+// strides (they may be views of one up-projection), k_shared [keys, R] with a row stride, R = 64 or 0.
+struct LatentArgs {
+    const __nv_bfloat16 *q, *k, *v, *r;
+    long long k_tok, k_head, v_tok, v_head, r_tok;   // strides in elements
+    const int32_t *cu_q, *cu_k;                      // null: B sequences of T queries and Tk keys
+    __nv_bfloat16 *out;
+    float *lse;
+    int B, T, Tk, H, N, R, causal;
+    float scale;
+    int32_t *status;
+};
+
+struct LatentSpan { long long q0, q1, k0, k1; };
+
+// Sequence n's queries [q0, q1) and keys [k0, k1). False for offsets that lie outside the tensors.
+__device__ __forceinline__ bool latent_span(const int32_t *cu_q, const int32_t *cu_k, int n, int T, int Tk, LatentSpan *s)
+{
+    if (cu_q) { s->q0 = cu_q[n]; s->q1 = cu_q[n + 1]; }
+    else { s->q0 = (long long)n * T; s->q1 = s->q0 + T; }
+    if (cu_k) { s->k0 = cu_k[n]; s->k1 = cu_k[n + 1]; }
+    else { s->k0 = (long long)n * Tk; s->k1 = s->k0 + Tk; }
+    if (cu_q && (s->q0 < 0 || s->q1 < s->q0 || s->q1 > T)) return false;
+    if (cu_k && (s->k0 < 0 || s->k1 < s->k0 || s->k1 > Tk)) return false;
+    return true;
+}
+
+// The sequence that holds token `tok` of offsets `cu` (or of B rows of T tokens), by bisection; -1 if none does.
+__device__ __forceinline__ int latent_sequence(const int32_t *cu, int N, int T, long long tok)
+{
+    if (!cu) return (int)(tok / T);
+    int lo = 0, hi = N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= tok) lo = mid; else hi = mid - 1;
+    }
+    return (cu[lo] <= tok && tok < cu[lo + 1]) ? lo : -1;
+}
+
+// Records offsets that break the contract (cu[0] = 0, non-decreasing, cu[N] = T). One block's threads.
+__device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T, int32_t *status)
+{
+    if (!cu) return;
+    for (int n = threadIdx.x; n < N; n += blockDim.x) {
+        const int a = cu[n], b = cu[n + 1];
+        if ((n == 0 && a != 0) || b < a || b > T || a < 0 || (n == N - 1 && b != T)) set_status(status, KDA_ERR_INVALID_ARG);
+    }
+}
+
+// Host checks of the expanded form's arguments, and the description they give.
+kda_status_t check_latent(const void *q, const void *k, const void *v, const void *k_shared, const int32_t *cu_q,
+                          const int32_t *cu_k, const void *out, const float *lse, int B, int T, int Tk, int H, int N,
+                          int dk, int dv, int dr, long long k_tok, long long k_head, long long v_tok, long long v_head,
+                          long long r_tok, float scale, kda_dtype_t dtype, const void *workspace, size_t workspace_bytes,
+                          size_t need, LatentArgs *a);
+
+cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
+
+struct LatentBwdArgs {
+    const __nv_bfloat16 *dout;
+    __nv_bfloat16 *dq, *dk, *dv, *dr;     // dense
+    float *delta;                         // [tokens, H]: dout . out
+    float *dr_head;                       // [keys, H, R]: each head's part of the shared key's gradient
+};
+cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaStream_t stream);
+
+}  // namespace kda
