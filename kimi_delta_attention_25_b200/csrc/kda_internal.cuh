@@ -178,6 +178,14 @@ struct GateArgs {
 bool token_rows_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint32_t elem_bytes, int H,
                     long long tokens, uint32_t box_cols = kHeadDim, bool swizzle128 = false);
 
+// Tensor maps of bf16 rows for tiles of box_rows rows by box_cols (64: the 128-byte swizzle) columns:
+// [rows][cols] with a row stride (2 coordinates: column, row), and [rows][heads][cols] with row and head
+// strides (heads > 1: 3 coordinates: column, row, head). Strides in elements.
+bool bf16_rows_map(CUtensorMap *m, const void *base, long long cols, long long rows, long long row_stride,
+                   uint32_t box_cols, uint32_t box_rows);
+bool bf16_heads_map(CUtensorMap *m, const void *base, long long cols, long long heads, long long rows,
+                    long long head_stride, long long row_stride, uint32_t box_cols, uint32_t box_rows);
+
 // Two-pass tensor-core chunk path for bf16 q/k/v: prepared operands go through the workspace.
 // (slots [slot_lo, slot_hi) only; slot_hi < 0: to the end)
 cudaError_t launch_chunk_prep(const PrefillArgs &a, unsigned char *ws, int n_slots, cudaStream_t stream,

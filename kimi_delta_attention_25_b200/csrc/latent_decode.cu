@@ -3,52 +3,572 @@
 // or none); every head reads the same rows, as keys and (the latent) as values:
 //   s_j = scale (q[:512] . c_j + q[512:] . r_j),   o = sum_j softmax_j(s) c_j   (512 values per head).
 // Token t of a sequence's Tq new ones (the last of its seq_len cached tokens) sees the rows up to its own.
-#include "kda_internal.cuh"
+//
+// What bounds it: the cache, 1152 bytes a row, read once; with 32 query rows that is 60 flops a byte, an
+// eighth of what the tensor cores could do meanwhile. So the kernel is built around the copies:
+//  - The queries of a sequence (Tq x H rows, in groups of at most 64) stay in shared memory, and the cache
+//    streams past them in tiles of 64 rows. One tile serves both products from the same shared memory: as
+//    K-major B operand of S = Q C^T and as MN-major A operand of O^T = C^T P^T. O^T (512 x rows, fp32) needs
+//    4 x rows tensor-memory columns, where O itself would need all 512 for any number of rows.
+//  - S runs with M = 128; with 64 query rows or fewer the upper lanes read whatever lies behind the queries
+//    in shared memory and are never looked at.
+//  - The tiles of all sequences form one list, cut into equal shares, one per SM (`lanes`), whatever the
+//    sequences' lengths. A sequence that a cut runs through leaves partial results (unnormalised O, maximum,
+//    sum, fp32), which a second kernel joins in order of the shares: no atomics, the same bits each time.
+//    The groups of one sequence (more than 64 rows) take the same share at the same time on neighbouring
+//    SMs, so that one of them finds the other's tile in L2.
+//  - The running maximum moves only when a row's scores pass it by more than 2^8 (P then stays below 2^8,
+//    exact in range for bf16, and l is fp32): the rescaling of O^T in tensor memory becomes rare.
+// P is rounded to bf16 as the operand of the second product; sums and statistics are fp32.
+#include "latent.cuh"
+#include "sm100.cuh"
 
 namespace kda {
 namespace {
 
+using namespace sm100;
+
+constexpr int KT = 64;                       // cache rows per tile
+constexpr int kLanes = 148;                  // shares of the list of tiles: one per SM of a B200
+constexpr int NSOFT = 256, NT = NSOFT + 64;  // softmax warps 0..7, loader 8, MMA issuer 9
+constexpr int W_LOAD = 8, W_MMA = 9;
+constexpr uint32_t SLOT = 16384;             // 64 cache rows x 128 latent channels: two 64-channel halves
+constexpr uint32_t SH_SLOT = 8192;           // 64 cache rows x the 64 shared channels
+
+// Shared memory for groups of RG query rows (16, 32 or 64): queries (9 chunks of 64 channels), P twice, the
+// shared key parts twice, and a ring of latent slots in what is left (a tile is four slots).
+template <int RG> struct Lay {
+    static constexpr uint32_t Q = 0, QCHUNK = RG * 128;
+    static constexpr uint32_t P = 9 * QCHUNK, PBUF = RG * 128 < 1024 ? 1024 : RG * 128;
+    static constexpr uint32_t SH = P + 2 * PBUF;
+    static constexpr uint32_t RING = SH + 2 * SH_SLOT;
+    static constexpr int NSLOT = RG == 64 ? 7 : 10;
+    static constexpr uint32_t MAXS = RING + NSLOT * SLOT;         // float [2][2][64]: by tile parity, each half's row maxima
+    static constexpr uint32_t LSUM = MAXS + 1024;                 // float [2][64]: each half's row sums
+    static constexpr uint32_t BAR = LSUM + 512;
+    static constexpr uint32_t TOTAL = BAR + 512 + 1024;           // with room to align the base
+    static_assert(TOTAL <= 232448, "shared memory");
+    static_assert(QCHUNK % 1024 == 0 && P % 1024 == 0, "swizzle atoms");
+    // the M = 128 product reads 128 rows from the start of each query chunk
+    static_assert(8 * QCHUNK + 128 * 128 <= MAXS, "queries' overread");
+};
+
 struct DecodeArgs {
-    const __nv_bfloat16 *q, *cache;
     const int32_t *table, *lens;
     __nv_bfloat16 *out;
     float *lse;
-    int N, Tq, H, R, page, pages, max_pages;
-    float scale;
+    int N, Tq, H, R, page, box, pages, max_pages;   // box: rows per copy (divides the page and the tile)
+    int G, L;                                       // groups of query rows, shares
+    float scale_log2;
+    float *part, *part_ml;                          // [L * G][2][RG][512], [L * G][2][RG][2]
+    int32_t *meta, *errs;                           // [L][2] {sequence cut at the share's end or -1, its last share}, [L * G]
     int32_t *status;
 };
 
-// One warp per (sequence, token, head).
-__global__ void __launch_bounds__(128) latent_decode_simple(DecodeArgs a)
+enum { B_QFULL, B_QEMPTY, B_SHFULL, B_SHEMPTY = B_SHFULL + 2, B_SFULL = B_SHEMPTY + 2, B_SFREE = B_SFULL + 2,
+       B_PREADY = B_SFREE + 2, B_PVDONE = B_PREADY + 2, B_FULL = B_PVDONE + 2, B_EMPTY = B_FULL + 10, B_DRAIN = B_EMPTY + 10,
+       N_BARS };
+static_assert(N_BARS * 8 + 64 <= 512, "barriers");
+
+__device__ __forceinline__ int tiles_of(const DecodeArgs &a, int n, int *len_out, bool *bad)
 {
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (long long)a.N * a.Tq * a.H) return;
-    const int n = (int)(row / ((long long)a.Tq * a.H)), t = (int)(row / a.H % a.Tq), W = kLatentDim + a.R;
-    long long len = a.lens[n];
-    if (len < 0 || len > (long long)a.max_pages * a.page) { set_status(a.status, KDA_ERR_INVALID_ARG); len = 0; }
-    float q[18], acc[16] = {}, m = -INFINITY, l = 0.f;
-    for (int c = 0; c < W / 32; ++c) q[c] = to_f32(a.q[row * W + c * 32 + lane]);
-    for (long long j = 0; j < len - a.Tq + t + 1; ++j) {
-        const int pg = a.table[(size_t)n * a.max_pages + j / a.page];
-        if (pg < 0 || pg >= a.pages) { set_status(a.status, KDA_ERR_INVALID_ARG); continue; }
-        const __nv_bfloat16 *c = a.cache + ((size_t)pg * a.page + j % a.page) * W;
-        float x[18], d = 0.f;
-        for (int i = 0; i < W / 32; ++i) { x[i] = to_f32(c[i * 32 + lane]); d += q[i] * x[i]; }
-        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        d *= a.scale;
-        const float m2 = fmaxf(m, d);
-        if (m2 == -INFINITY) continue;
-        const float f = expf(m - m2), p = expf(d - m2);
-        l = l * f + p;
-        for (int i = 0; i < 16; ++i) acc[i] = acc[i] * f + p * x[i];
-        m = m2;
+    const int len = a.lens[n];
+    if (len < 0 || (long long)len > (long long)a.max_pages * a.page) { *bad = true; *len_out = 0; return 0; }
+    *len_out = len;
+    return (len + KT - 1) / KT;
+}
+
+template <int RG>
+__global__ void __launch_bounds__(NT, 1)
+latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c)
+{
+    using Y = Lay<RG>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int share = blockIdx.x / a.G, g = blockIdx.x % a.G;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Y::BAR);
+    volatile int *ctl = reinterpret_cast<volatile int *>(bars + N_BARS);   // [0] tmem, [1] abort, [2] error, [3] n0, [4] off0
+    __shared__ long long s_scan[NT], s_prefix;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
+    if (tid == 0) {
+        mbar_init(&bars[B_QFULL], 1);
+        mbar_init(&bars[B_QEMPTY], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[B_SHFULL + i], 1);
+            mbar_init(&bars[B_SHEMPTY + i], 1);
+            mbar_init(&bars[B_SFULL + i], 1);
+            mbar_init(&bars[B_SFREE + i], 8);
+            mbar_init(&bars[B_PREADY + i], 8);
+            mbar_init(&bars[B_PVDONE + i], 1);
+        }
+        for (int i = 0; i < Y::NSLOT; ++i) { mbar_init(&bars[B_FULL + i], 1); mbar_init(&bars[B_EMPTY + i], 1); }
+        mbar_init(&bars[B_DRAIN], 1);
+        ctl[1] = 0; ctl[2] = 0; ctl[3] = a.N; ctl[4] = 0; s_prefix = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_c);
     }
-    for (int i = 0; i < 16; ++i) a.out[row * kLatentDim + i * 32 + lane] = __float2bfloat16_rn(l > 0.f ? acc[i] / l : 0.f);
-    if (lane == 0) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+    // The list of tiles: each thread counts a run of sequences, then finds whether this share begins in it.
+    const int per = (a.N + NT - 1) / NT, n_lo = min(a.N, tid * per), n_hi = min(a.N, n_lo + per);
+    bool bad = false;
+    long long mine = 0;
+    for (int n = n_lo; n < n_hi; ++n) { int len; mine += tiles_of(a, n, &len, &bad); }
+    s_scan[tid] = mine;
+    __syncthreads();
+    for (int o = 1; o < NT; o <<= 1) {
+        const long long v = tid >= o ? s_scan[tid - o] : 0;
+        __syncthreads();
+        s_scan[tid] += v;
+        __syncthreads();
+    }
+    const long long total = s_scan[NT - 1];
+    // shares that get tiles: with fewer tiles than shares one each, so that no share inside a cut sequence is empty
+    const int used = (int)min((long long)a.L, total);
+    const long long begin = share < used ? total * share / used : 0, end = share < used ? total * (share + 1) / used : 0;
+    {
+        long long at = s_scan[tid] - mine;
+        if (begin >= at && begin < at + mine && begin < end)
+            for (int n = n_lo; n < n_hi; ++n) {
+                int len;
+                const int t = tiles_of(a, n, &len, &bad);
+                if (begin < at + t) { ctl[3] = n; ctl[4] = (int)(begin - at); s_prefix = at; break; }
+                at += t;
+            }
+    }
+    if (bad) ctl[2] = KDA_ERR_INVALID_ARG;
+    const int rows = min(RG, a.Tq * a.H - g * RG);             // this group's query rows
+    for (int n = share; n < a.N; n += a.L) {                   // idle slots: nothing to attend to
+        int len;
+        if (tiles_of(a, n, &len, &bad) == 0) {
+            const size_t r0 = (size_t)n * a.Tq * a.H + g * RG;
+            for (int i = tid; i < rows * (kLatentDim / 8); i += NT)
+                reinterpret_cast<uint4 *>(a.out + r0 * kLatentDim)[i] = make_uint4(0, 0, 0, 0);
+            for (int i = tid; i < rows; i += NT) a.lse[r0 + i] = -INFINITY;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
+    const uint32_t TM_O = tmem + 128;
+    const int n0 = ctl[3], off0 = ctl[4];
+    const int chunks = 8 + (a.R ? 1 : 0);
+
+    volatile int *abort_flag = ctl + 1;
+    auto wait = [&](int b, uint32_t parity) {
+        if (mbar_try_wait(&bars[b], parity)) return true;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&bars[b], parity)) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > 2000000000LL) { *abort_flag = 1; ctl[2] = KDA_ERR_TIMEOUT; return false; }
+        }
+        return true;
+    };
+
+    if (warp == W_LOAD) {
+        // ============================================================================ loader
+        // The warp's lanes share a tile's copies: one per 64-channel half and box of rows.
+        const int nb = KT / a.box, b = lane % nb;
+        int it = 0, seg = 0, n = n0, off = off0, slots_used = 0;
+        long long left = end - begin;
+        bool ok = true;
+        while (left > 0 && ok) {
+            int len;
+            bool x = false;
+            const int tiles = tiles_of(a, n, &len, &x), cnt = (int)min((long long)(tiles - off), left);
+            if (cnt <= 0) { ++n; off = 0; continue; }
+            // the sequence's queries, once the last segment's scores are done
+            if (seg > 0) ok = wait(B_QEMPTY, (seg - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive_expect_tx(&bars[B_QFULL], chunks * Y::QCHUNK);
+            __syncwarp();
+            if (lane < chunks) tma_load_2d(sm + Y::Q + lane * Y::QCHUNK, &tm_q, &bars[B_QFULL], lane * 64, n * a.Tq * a.H + g * RG);
+            // row coordinate of this lane's box in tile t; behind the last row, or on a page that is not there, the
+            // copy starts behind the cache and reads zeros
+            auto coord = [&](int t) {
+                const int row = t * KT + b * a.box;
+                if (row >= len) return a.pages * a.page;
+                const int pg = a.table[(size_t)n * a.max_pages + row / a.page];
+                if (pg < 0 || pg >= a.pages) { ctl[2] = KDA_ERR_INVALID_ARG; return a.pages * a.page; }
+                return pg * a.page + row % a.page;
+            };
+            int next = coord(off);
+            for (int t = off; t < off + cnt && ok; ++t, ++it) {
+                const int c1 = next;
+                if (t + 1 < off + cnt) next = coord(t + 1);
+                if (a.R) {
+                    const int s = it & 1;
+                    if (it >= 2) ok = wait(B_SHEMPTY + s, ((it >> 1) - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars[B_SHFULL + s], SH_SLOT);
+                    __syncwarp();
+                    if (lane < nb) tma_load_2d(sm + Y::SH + s * SH_SLOT + b * a.box * 128, &tm_c, &bars[B_SHFULL + s], kLatentDim, c1);
+                }
+                for (int c = 0; c < 4; ++c) {
+                    const int i = it * 4 + c, s = i % Y::NSLOT, use = i / Y::NSLOT;
+                    if (use > 0) ok = wait(B_EMPTY + s, (use - 1) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(&bars[B_FULL + s], SLOT);
+                    __syncwarp();
+                    const int half = lane / nb;
+                    if (half < 2) tma_load_2d(sm + Y::RING + s * SLOT + half * 8192 + b * a.box * 128, &tm_c, &bars[B_FULL + s], c * 128 + half * 64, c1);
+                    slots_used = i + 1;
+                }
+            }
+            ++seg; left -= cnt; ++n; off = 0;
+        }
+        // copies still in flight (only after a wait ran out) land before the block ends
+        if (!ok && lane == 0) {
+            if (seg >= 0 && left > 0) for (int i = 0; i < 100 && !mbar_wait(&bars[B_QFULL], seg & 1, 1000000LL); ++i) {}
+            for (int i = max(0, slots_used - Y::NSLOT); i < slots_used; ++i)
+                mbar_wait(&bars[B_FULL + i % Y::NSLOT], (i / Y::NSLOT) & 1, 100000000LL);
+            if (a.R) for (int i = max(0, it - 1); i <= it; ++i) mbar_wait(&bars[B_SHFULL + (i & 1)], (i >> 1) & 1, 100000000LL);
+        }
+    } else if (warp == W_MMA) {
+        // ======================================================================== MMA issuer
+        // One thread runs both products as their operands arrive: scores of a tile slot by slot while its
+        // copies land, the second product of the tile before as soon as its P is there.
+        if (lane == 0) {
+            const uint32_t id_s = idesc_bf16(128, KT, 0, 0), id_o = idesc_bf16(128, RG, 1, 0);
+            const long long ntile = end - begin;
+            int n = n0, off = off0, seg = 0, seg_left = 0, seg_first = 1;
+            long long js = 0, jp = 0;          // next tile of the scores, of the second product
+            int u = 0;                         // next operand of the scores' tile: 0 checks, 1 shared part, 2..5 latent slots
+            // first tiles of segments, for the second product's accumulate flag (by tile modulo 8: at most three are pending)
+            uint32_t first_bits = 0;
+            long long t0 = clock64();
+            bool ok = true;
+            while (jp < ntile) {
+                bool moved = false;
+                if (jp < js && mbar_try_wait(&bars[B_PREADY + (jp & 1)], (jp >> 1) & 1)) {
+                    tc_fence_after();
+                    const bool first = (first_bits >> (jp & 7)) & 1;
+                    const uint32_t pb = sbase + Y::P + (uint32_t)(jp & 1) * Y::PBUF;
+                    for (int c = 0; c < 4; ++c) {
+                        const int s = (int)((jp * 4 + c) % Y::NSLOT);
+                        const uint32_t slot = sbase + Y::RING + s * SLOT;
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_ss(TM_O + c * RG, smem_desc(slot + ks * 2048, 8192, 1024, SW_128B),
+                                    smem_desc(pb + ks * 32, 16, 1024, SW_128B), id_o, (ks > 0 || !first) ? 1 : 0);
+                        umma_commit(&bars[B_EMPTY + s]);
+                    }
+                    umma_commit(&bars[B_PVDONE + (jp & 1)]);
+                    ++jp;
+                    moved = true;
+                } else if (js < ntile) {
+                    const uint32_t d = tmem + (uint32_t)(js & 1) * 64;
+                    if (u == 0) {
+                        // the buffer of S is free, and at a segment's start its queries are there
+                        if (js < 2 || mbar_try_wait(&bars[B_SFREE + (js & 1)], ((js >> 1) - 1) & 1)) {
+                            if (seg_left == 0) {
+                                int len, tiles;
+                                bool x = false;
+                                while ((tiles = tiles_of(a, n, &len, &x) - off) <= 0) { ++n; off = 0; }
+                                seg_left = (int)min((long long)tiles, ntile - js);
+                                seg_first = 1;
+                            }
+                            if (!seg_first || mbar_try_wait(&bars[B_QFULL], seg & 1)) { u = a.R ? 1 : 2; moved = true; }
+                        }
+                    } else if (u == 1) {
+                        const int s = (int)(js & 1);
+                        if (mbar_try_wait(&bars[B_SHFULL + s], (js >> 1) & 1)) {
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                umma_ss(d, smem_desc(sbase + Y::Q + 8 * Y::QCHUNK + ks * 32, 16, 1024, SW_128B),
+                                        smem_desc(sbase + Y::SH + s * SH_SLOT + ks * 32, 16, 1024, SW_128B), id_s, ks > 0);
+                            umma_commit(&bars[B_SHEMPTY + s]);
+                            u = 2;
+                            moved = true;
+                        }
+                    } else {
+                        const int c = u - 2;
+                        const long long i = js * 4 + c;
+                        const int s = (int)(i % Y::NSLOT);
+                        if (mbar_try_wait(&bars[B_FULL + s], (uint32_t)(i / Y::NSLOT) & 1)) {
+                            tc_fence_after();
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks)
+                                umma_ss(d, smem_desc(sbase + Y::Q + (2 * c + (ks >> 2)) * Y::QCHUNK + (ks & 3) * 32, 16, 1024, SW_128B),
+                                        smem_desc(sbase + Y::RING + s * SLOT + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024, SW_128B),
+                                        id_s, (a.R || c > 0 || ks > 0) ? 1 : 0);
+                            moved = true;
+                            if (++u == 6) {
+                                umma_commit(&bars[B_SFULL + (js & 1)]);
+                                first_bits = (first_bits & ~(1u << (js & 7))) | ((uint32_t)seg_first << (js & 7));
+                                seg_first = 0;
+                                if (--seg_left == 0) { umma_commit(&bars[B_QEMPTY]); ++seg; ++n; off = 0; }
+                                u = 0;
+                                ++js;
+                            }
+                        }
+                    }
+                }
+                if (moved) { t0 = clock64(); continue; }
+                if (*abort_flag) { ok = false; break; }
+                if (clock64() - t0 > 2000000000LL) { *abort_flag = 1; ctl[2] = KDA_ERR_TIMEOUT; ok = false; break; }
+            }
+            (void)ok;
+            umma_commit(&bars[B_DRAIN]);
+            if (!mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) ctl[2] = KDA_ERR_TIMEOUT;
+        }
+    } else {
+        // ============================================================================ softmax
+        // Warp w reads tensor-memory lanes 32 (w % 4) ..: for S the query rows (warps with w % 4 < RG / 32),
+        // columns 32 (w / 4) .. of the tile; for O^T the latent channels of chunks 2 (w / 4) and 2 (w / 4) + 1.
+        const int quad = warp & 3, half = warp >> 2;
+        const uint32_t lanes = (uint32_t)quad << 21;
+        const bool active = quad < (RG == 64 ? 2 : 1);
+        float *smax = reinterpret_cast<float *>(sm + Y::MAXS), *slsum = reinterpret_cast<float *>(sm + Y::LSUM);
+        const int row = quad * 32 + lane;                    // active warps: this thread's query row
+        const bool real = active && row < rows;
+        const int tq = real ? (g * RG + row) / a.H : 0;
+        long long j = 0;                                     // tile of this share
+        int n = n0, off = off0;
+        long long left = end - begin, pfx = s_prefix;        // pfx: tiles before sequence n
+        int cut_n = -1, cut_last = 0;
+        while (left > 0) {
+            int len;
+            bool x = false;
+            const int tiles = tiles_of(a, n, &len, &x), cnt = (int)min((long long)(tiles - off), left);
+            if (cnt <= 0) { ++n; off = 0; continue; }
+            const int lim = real ? max(0, len - a.Tq + tq + 1) : 0;
+            // every warp keeps the running maxima of rows `lane` and `lane + 32` (log2 domain)
+            float m_lo = -INFINITY, m_hi = -INFINITY, lsum = 0.f;
+            for (int t = off; t < off + cnt; ++t, ++j) {
+                const int buf = (int)(j & 1);
+                wait(B_SFULL + buf, (uint32_t)(j >> 1) & 1);
+                __syncwarp();
+                tc_fence_after();
+                float s[32];
+                if (active) {
+                    tmem_ld32_sync(tmem + lanes + buf * 64 + half * 32, s);
+                    tc_fence_before();
+                }
+                __syncwarp();
+                // every warp, so that none can still be waiting for this phase when the buffer's next one ends
+                if (lane == 0) mbar_arrive(&bars[B_SFREE + buf]);
+                float *mx_tile = smax + buf * 128;
+                if (active) {
+                    const int k0 = t * KT + half * 32;
+                    float mx = -INFINITY;
+                    if (k0 + 32 <= lim) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) { s[i] *= a.scale_log2; mx = fmaxf(mx, s[i]); }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) { s[i] = k0 + i < lim ? s[i] * a.scale_log2 : -INFINITY; mx = fmaxf(mx, s[i]); }
+                    }
+                    mx_tile[half * 64 + row] = mx;
+                }
+                // rows of the tile behind the sequence's end may hold anything: zeros, as values
+                const int valid = len - t * KT;
+                if (valid < KT) {
+                    for (int c = 0; c < 4; ++c) {
+                        unsigned char *slot = sm + Y::RING + (uint32_t)((j * 4 + c) % Y::NSLOT) * SLOT;
+                        for (int i = warp * 32 + lane; i < 2 * (KT - valid) * 8; i += NSOFT) {
+                            const int hf = i / ((KT - valid) * 8), o = i % ((KT - valid) * 8);
+                            *reinterpret_cast<uint4 *>(slot + hf * 8192 + valid * 128 + o * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                named_bar_sync(1, NSOFT);
+                const float c_lo = fmaxf(mx_tile[lane], mx_tile[64 + lane]);
+                const float c_hi = RG == 64 ? fmaxf(mx_tile[32 + lane], mx_tile[96 + lane]) : -INFINITY;
+                const bool up = c_lo > m_lo + 8.f || c_hi > m_hi + 8.f;
+                if (__any_sync(0xffffffffu, up)) {           // the same outcome in all warps
+                    const float q_lo = fmaxf(m_lo, c_lo), q_hi = fmaxf(m_hi, c_hi);
+                    const float f_lo = q_lo == m_lo ? 1.f : exp2f(m_lo - q_lo), f_hi = q_hi == m_hi ? 1.f : exp2f(m_hi - q_hi);
+                    m_lo = q_lo; m_hi = q_hi;
+                    if (active) lsum *= (quad & 1) ? f_hi : f_lo;
+                    if (t > off) {
+                        wait(B_PVDONE + (buf ^ 1), (uint32_t)((j - 1) >> 1) & 1);
+                        __syncwarp();
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                            for (int q = 0; q < RG / 16; ++q) {
+                                const uint32_t ad = TM_O + lanes + (2 * half + c) * RG + q * 16;
+                                float o[16];
+                                tmem_ld16_sync(ad, o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    o[i] *= __shfl_sync(0xffffffffu, q < 2 ? f_lo : f_hi, (q & 1) * 16 + i);
+                                tmem_st16(ad, o);
+                            }
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                    }
+                }
+                if (active) {
+                    const float m = (quad & 1) ? m_hi : m_lo;
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    // P's buffer was last read by the second product of tile j - 2
+                    if (j >= 2) { wait(B_PVDONE + buf, (uint32_t)((j >> 1) - 1) & 1); __syncwarp(); }
+                    unsigned char *pr = sm + Y::P + buf * Y::PBUF + row * 128;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float p0 = ex2(s[8 * c + 2 * i] - mu), p1 = ex2(s[8 * c + 2 * i + 1] - mu);
+                            lsum += p0 + p1;
+                            w[i] = pack_bf16x2(p0, p1);
+                        }
+                        if (row < RG) *reinterpret_cast<uint4 *>(pr + (((half * 4 + c) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[B_PREADY + buf]);
+            }
+            // -------- the segment's results
+            if (active) slsum[half * 64 + row] = lsum;
+            const long long jl = j - 1;
+            wait(B_PVDONE + (jl & 1), (uint32_t)(jl >> 1) & 1);
+            __syncwarp();
+            tc_fence_after();
+            named_bar_sync(1, NSOFT);
+            const float l_lo = slsum[lane] + slsum[64 + lane], l_hi = RG == 64 ? slsum[32 + lane] + slsum[96 + lane] : 0.f;
+            const bool whole = off == 0 && cnt == tiles;
+            const float i_lo = whole ? (l_lo > 0.f ? 1.f / l_lo : (l_lo == 0.f ? 0.f : l_lo)) : 1.f;
+            const float i_hi = whole ? (l_hi > 0.f ? 1.f / l_hi : (l_hi == 0.f ? 0.f : l_hi)) : 1.f;
+            const size_t r0 = (size_t)n * a.Tq * a.H + g * RG;
+            const size_t pslot = (size_t)blockIdx.x * 2 + (off == 0 ? 1 : 0);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int dim = (2 * half + c) * 128 + quad * 32 + lane;
+#pragma unroll
+                for (int q = 0; q < RG / 16; ++q) {
+                    float o[16];
+                    tmem_ld16_sync(TM_O + lanes + (2 * half + c) * RG + q * 16, o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float v = o[i] * __shfl_sync(0xffffffffu, q < 2 ? i_lo : i_hi, (q & 1) * 16 + i);
+                        const int r = q * 16 + i;
+                        if (r < rows) {
+                            if (whole) a.out[(r0 + r) * kLatentDim + dim] = __float2bfloat16_rn(v);
+                            else a.part[(pslot * RG + r) * kLatentDim + dim] = v;
+                        }
+                    }
+                }
+            }
+            if (warp == 0) {
+#pragma unroll
+                for (int i = 0; i < (RG == 64 ? 2 : 1); ++i) {
+                    const int r = lane + 32 * i;
+                    const float m = i ? m_hi : m_lo, l = i ? l_hi : l_lo;
+                    if (r < rows) {
+                        if (whole) a.lse[r0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                        else *reinterpret_cast<float2 *>(a.part_ml + (pslot * RG + r) * 2) = make_float2(m, l);
+                    }
+                }
+            }
+            if (!whole && off == 0) {                        // cut at this share's end: who joins it
+                cut_n = n;
+                const long long last = pfx + tiles - 1;
+                cut_last = (int)(((last + 1) * used - 1) / total);
+            }
+            tc_fence_before();
+            named_bar_sync(1, NSOFT);                        // the sums and O are read before the next segment
+            left -= cnt; pfx += tiles; ++n; off = 0;
+        }
+        if (tid == 0 && g == 0) { a.meta[2 * share] = cut_n; a.meta[2 * share + 1] = cut_last; }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0) a.errs[blockIdx.x] = ctl[2];
+    if (warp == W_MMA) tmem_dealloc(tmem, 512);
+}
+
+// Joins the partial results of each sequence that a cut runs through: block (share, group) x row, for the
+// sequence whose first part lies at the end of that share. The first block also gathers the blocks' errors
+// into the status word.
+template <int RG>
+__global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int share = blockIdx.x / a.G, g = blockIdx.x % a.G, r = blockIdx.y;
+    if (blockIdx.x == 0 && r == 0) {
+        int err = 0;
+        for (int i = threadIdx.x; i < a.L * a.G; i += 128) err = max(err, a.errs[i]);
+        err = __syncthreads_or(err == KDA_ERR_TIMEOUT) ? KDA_ERR_TIMEOUT : (__syncthreads_or(err) ? KDA_ERR_INVALID_ARG : 0);
+        if (threadIdx.x == 0) *a.status = err;
+    }
+    const int n = a.meta[2 * share], last = a.meta[2 * share + 1];
+    if (n < 0 || g * RG + r >= a.Tq * a.H) return;
+    auto slot_of = [&](int s) { return ((size_t)(s * a.G + g) * 2 + (s == share ? 1 : 0)) * RG + r; };
+    float m = -INFINITY;
+    for (int s = share; s <= last; ++s) m = fmaxf(m, a.part_ml[slot_of(s) * 2]);
+    const float mu = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = share; s <= last; ++s) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot_of(s) * 2);
+        const float f = exp2f(ml.x - mu);
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(s) * kLatentDim) + threadIdx.x);
+        l += f * ml.y;
+        o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const size_t row = (size_t)n * a.Tq * a.H + g * RG + r;
+    reinterpret_cast<uint2 *>(a.out + row * kLatentDim)[threadIdx.x] =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 bool al(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Rows per group, groups and shares for Tq x H query rows.
+struct Plan { int RG, G, L; size_t meta, errs, part, ml, total; };
+Plan plan_of(long long rows)
+{
+    Plan p;
+    p.RG = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.G = (int)((rows + p.RG - 1) / p.RG);
+    p.L = p.G >= kLanes ? 1 : kLanes / p.G;
+    size_t off = kStatusBytes;
+    p.meta = off; off += align256((size_t)p.L * 8);
+    p.errs = off; off += align256((size_t)p.L * p.G * 4);
+    p.ml = off; off += align256((size_t)p.L * p.G * 2 * p.RG * 8);
+    p.part = off; off += (size_t)p.L * p.G * 2 * p.RG * kLatentDim * 4;
+    p.total = off;
+    return p;
+}
+
+template <int RG>
+cudaError_t launch(const DecodeArgs &a, const CUtensorMap &tq, const CUtensorMap &tc, cudaStream_t st)
+{
+    auto kern = latent_decode_kernel<RG>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<RG>::TOTAL);
+    if (e != cudaSuccess) return e;
+    kern<<<a.L * a.G, NT, Lay<RG>::TOTAL, st>>>(a, tq, tc);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // the join's blocks may be scheduled while the last shares finish; they wait for the whole first kernel
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.L * a.G, RG < a.Tq * a.H ? RG : a.Tq * a.H);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_decode_join<RG>, a);
+}
 
 }  // namespace
 }  // namespace kda
@@ -59,8 +579,8 @@ extern "C" {
 
 size_t kda_latent_decode_workspace_size(int N, int Tq, int H)
 {
-    if (N < 0 || Tq < 1 || H < 1) return 0;
-    return kStatusBytes;
+    if (N < 0 || Tq < 1 || H < 1 || (long long)Tq * H > 65536) return 0;
+    return plan_of((long long)Tq * H).total;
 }
 
 kda_status_t kda_latent_decode_step(const void *q, const void *cache, const int32_t *page_table, const int32_t *seq_lens,
@@ -71,27 +591,36 @@ kda_status_t kda_latent_decode_step(const void *q, const void *cache, const int3
     if (dtype != KDA_F32 && dtype != KDA_BF16) return KDA_ERR_INVALID_ARG;
     if (N < 0 || Tq < 1 || H < 1 || page_size < 1 || num_pages < 0 || max_pages < 0) return KDA_ERR_INVALID_ARG;
     if (!(scale > 0.f) || scale > 3.0e38f) return KDA_ERR_INVALID_ARG;
-    if (!workspace || !al(workspace, 16) || workspace_bytes < kda_latent_decode_workspace_size(N, Tq, H)) return KDA_ERR_INVALID_ARG;
     if (dtype != KDA_BF16 || dc != kLatentDim || (dr != 0 && dr != kSharedDim) || page_size % 16 != 0) return KDA_ERR_UNSUPPORTED;
-    if (num_pages * page_size > 0x7fffffffLL || (long long)max_pages * page_size > 0x7fffffffLL ||
-        (long long)N * Tq * H > 0x7fffffffLL || N > kMaxGridDim)
+    if (num_pages * page_size > 0x7fff0000LL || (long long)max_pages * page_size > 0x7fff0000LL ||
+        (long long)Tq * H > 65536 || (long long)N * Tq * H > 0x7fff0000LL || N > kMaxGridDim)
         return KDA_ERR_UNSUPPORTED;
+    if (!workspace || !al(workspace, 16) || workspace_bytes < kda_latent_decode_workspace_size(N, Tq, H)) return KDA_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;
-    if (N > 0) {
-        if (!q || !seq_lens || !out || !lse) return KDA_ERR_INVALID_ARG;
-        if (!al(q, 16) || !al(cache, 16) || !al(page_table, 4) || !al(seq_lens, 4) || !al(out, 16) || !al(lse, 4))
-            return KDA_ERR_INVALID_ARG;
-        if (max_pages > 0 && (!page_table || (num_pages > 0 && !cache))) return KDA_ERR_INVALID_ARG;
-    }
-    if (cudaMemsetAsync(workspace, 0, kStatusBytes, st) != cudaSuccess) return KDA_ERR_CUDA;
-    if (N == 0) return KDA_OK;
+    if (N == 0) return cudaMemsetAsync(workspace, 0, kStatusBytes, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    if (!q || !seq_lens || !out || !lse) return KDA_ERR_INVALID_ARG;
+    if (!al(q, 16) || !al(cache, 16) || !al(page_table, 4) || !al(seq_lens, 4) || !al(out, 16) || !al(lse, 4))
+        return KDA_ERR_INVALID_ARG;
+    if (max_pages > 0 && (!page_table || (num_pages > 0 && !cache))) return KDA_ERR_INVALID_ARG;
+    const Plan pl = plan_of((long long)Tq * H);
+    unsigned char *ws = (unsigned char *)workspace;
     DecodeArgs a;
-    a.q = (const __nv_bfloat16 *)q; a.cache = (const __nv_bfloat16 *)cache; a.table = page_table; a.lens = seq_lens;
-    a.out = (__nv_bfloat16 *)out; a.lse = lse; a.N = N; a.Tq = Tq; a.H = H; a.R = dr; a.page = page_size;
-    a.pages = (int)num_pages; a.max_pages = max_pages; a.scale = scale; a.status = (int32_t *)workspace;
-    const long long rows = (long long)N * Tq * H;
-    latent_decode_simple<<<(unsigned)((rows + 3) / 4), 128, 0, st>>>(a);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    a.table = page_table; a.lens = seq_lens; a.out = (__nv_bfloat16 *)out; a.lse = lse;
+    a.N = N; a.Tq = Tq; a.H = H; a.R = dr; a.page = page_size; a.pages = (int)num_pages; a.max_pages = max_pages;
+    a.box = KT;
+    while (page_size % a.box) a.box >>= 1;                     // 64, 32 or 16
+    a.G = pl.G; a.L = pl.L; a.scale_log2 = scale * 1.44269504088896341f;
+    a.meta = (int32_t *)(ws + pl.meta); a.errs = (int32_t *)(ws + pl.errs);
+    a.part_ml = (float *)(ws + pl.ml); a.part = (float *)(ws + pl.part);
+    a.status = (int32_t *)ws;
+    const long long W = kLatentDim + dr, qrows = (long long)N * Tq * H, crows = num_pages * page_size;
+    // without a cache row every length is idle (or refused on the device), and no copy is made
+    CUtensorMap tq = {}, tc = {};
+    if (crows > 0 && (!bf16_rows_map(&tq, q, W, qrows, W, 64, pl.RG) || !bf16_rows_map(&tc, cache, W, crows, W, 64, a.box)))
+        return KDA_ERR_CUDA;
+    if (crows == 0) a.max_pages = 0;
+    const cudaError_t e = pl.RG == 16 ? launch<16>(a, tq, tc, st) : pl.RG == 32 ? launch<32>(a, tq, tc, st) : launch<64>(a, tq, tc, st);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"
