@@ -173,7 +173,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         // ============================================================================ loader
         // The warp's lanes share a tile's copies: one per 64-channel half and box of rows.
         const int nb = KT / a.box, b = lane % nb;
-        int it = 0, seg = 0, n = n0, off = off0, slots_used = 0;
+        int it = 0, seg = 0, n = n0, off = off0, slots_used = 0, slot_next = 0, slot_phase = 0;
         long long left = end - begin;
         bool ok = true;
         while (left > 0 && ok) {
@@ -190,17 +190,19 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
             if (lane < chunks) tma_load_2d(sm + Y::Q + lane * Y::QCHUNK, &tm_q, &bars[B_QFULL], lane * 64, n * a.Tq * a.H + g * RG);
             // row coordinate of this lane's box in tile t; behind the last row, or on a page that is not there, the
             // copy starts behind the cache and reads zeros
-            auto coord = [&](int t) {
-                const int row = t * KT + b * a.box;
-                if (row >= len) return a.pages * a.page;
-                const int pg = a.table[(size_t)n * a.max_pages + row / a.page];
-                if (pg < 0 || pg >= a.pages) { ctl[2] = KDA_ERR_INVALID_ARG; return a.pages * a.page; }
-                return pg * a.page + row % a.page;
-            };
-            int next = coord(off);
+            // (the table's entry is read a tile ahead and looked at when its turn comes)
+            int row = off * KT + b * a.box, pi = row / a.page, po = row % a.page;
+            const int32_t *tab = a.table + (size_t)n * a.max_pages;
+            int entry = row < len ? tab[pi] : 0;
             for (int t = off; t < off + cnt && ok; ++t, ++it) {
-                const int c1 = next;
-                if (t + 1 < off + cnt) next = coord(t + 1);
+                int c1 = a.pages * a.page;
+                if (row < len) {
+                    if (entry >= 0 && entry < a.pages) c1 = entry * a.page + po;
+                    else ctl[2] = KDA_ERR_INVALID_ARG;
+                }
+                row += KT; po += KT;
+                while (po >= a.page) { po -= a.page; ++pi; }
+                if (row < len) entry = tab[pi];
                 if (a.R) {
                     const int s = it & 1;
                     if (it >= 2) ok = wait(B_SHEMPTY + s, ((it >> 1) - 1) & 1);
@@ -211,8 +213,8 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                     if (lane < nb) tma_load_2d(sm + Y::SH + s * SH_SLOT + b * a.box * 128, &tm_c, &bars[B_SHFULL + s], kLatentDim, c1);
                 }
                 for (int c = 0; c < 4; ++c) {
-                    const int i = it * 4 + c, s = i % Y::NSLOT, use = i / Y::NSLOT;
-                    if (use > 0) ok = wait(B_EMPTY + s, (use - 1) & 1);
+                    const int i = slots_used, s = slot_next;
+                    if (i >= Y::NSLOT) ok = wait(B_EMPTY + s, slot_phase ^ 1);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(&bars[B_FULL + s], SLOT);
@@ -220,6 +222,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                     const int half = lane / nb;
                     if (half < 2) tma_load_2d(sm + Y::RING + s * SLOT + half * 8192 + b * a.box * 128, &tm_c, &bars[B_FULL + s], c * 128 + half * 64, c1);
                     slots_used = i + 1;
+                    if (++slot_next == Y::NSLOT) { slot_next = 0; slot_phase ^= 1; }
                 }
             }
             ++seg; left -= cnt; ++n; off = 0;
@@ -235,30 +238,36 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         // ======================================================================== MMA issuer
         // One thread runs both products as their operands arrive: scores of a tile slot by slot while its
         // copies land, the second product of the tile before as soon as its P is there.
-        if (lane == 0) {
-            const uint32_t id_s = idesc_bf16(128, KT, 0, 0), id_o = idesc_bf16(128, RG, 1, 0);
+        if (elect_one()) {
+            constexpr uint32_t id_s = idesc_bf16(128, KT, 0, 0), id_o = idesc_bf16(128, RG, 1, 0);
+            constexpr uint32_t hi = desc_hi(1024, SW_128B);
+            // K-major operands (queries, cache rows as keys, P) and the cache rows as MN-major values
+            const uint32_t q_lo = desc_lo(sbase + Y::Q, 16), p_lo = desc_lo(sbase + Y::P, 16), sh_lo = desc_lo(sbase + Y::SH, 16);
+            const uint32_t k_lo = desc_lo(sbase + Y::RING, 16), v_lo = desc_lo(sbase + Y::RING, 8192);
             const long long ntile = end - begin;
             int n = n0, off = off0, seg = 0, seg_left = 0, seg_first = 1;
             long long js = 0, jp = 0;          // next tile of the scores, of the second product
             int u = 0;                         // next operand of the scores' tile: 0 checks, 1 shared part, 2..5 latent slots
             // first tiles of segments, for the second product's accumulate flag (by tile modulo 8: at most three are pending)
             uint32_t first_bits = 0;
+            int ps = 0, ks_slot = 0;           // ring slots of the second product and of the scores
+            uint32_t ks_phase = 0;
             long long t0 = clock64();
             bool ok = true;
             while (jp < ntile) {
                 bool moved = false;
-                if (jp < js && mbar_try_wait(&bars[B_PREADY + (jp & 1)], (jp >> 1) & 1)) {
+                if (jp < js && mbar_test_wait(&bars[B_PREADY + (jp & 1)], (jp >> 1) & 1)) {
                     tc_fence_after();
-                    const bool first = (first_bits >> (jp & 7)) & 1;
-                    const uint32_t pb = sbase + Y::P + (uint32_t)(jp & 1) * Y::PBUF;
+                    const uint32_t more = ((first_bits >> (jp & 7)) & 1) ^ 1u;
+                    const uint32_t pb = p_lo + (uint32_t)(jp & 1) * (Y::PBUF / 16);
+#pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int s = (int)((jp * 4 + c) % Y::NSLOT);
-                        const uint32_t slot = sbase + Y::RING + s * SLOT;
+                        const uint32_t slot = v_lo + ps * (SLOT / 16);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            umma_ss(TM_O + c * RG, smem_desc(slot + ks * 2048, 8192, 1024, SW_128B),
-                                    smem_desc(pb + ks * 32, 16, 1024, SW_128B), id_o, (ks > 0 || !first) ? 1 : 0);
-                        umma_commit(&bars[B_EMPTY + s]);
+                            umma_ss(TM_O + c * RG, desc64(slot + ks * 128, hi), desc64(pb + ks * 2, hi), id_o, ks > 0 ? 1 : more);
+                        umma_commit(&bars[B_EMPTY + ps]);
+                        if (++ps == Y::NSLOT) ps = 0;
                     }
                     umma_commit(&bars[B_PVDONE + (jp & 1)]);
                     ++jp;
@@ -267,7 +276,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                     const uint32_t d = tmem + (uint32_t)(js & 1) * 64;
                     if (u == 0) {
                         // the buffer of S is free, and at a segment's start its queries are there
-                        if (js < 2 || mbar_try_wait(&bars[B_SFREE + (js & 1)], ((js >> 1) - 1) & 1)) {
+                        if (js < 2 || mbar_test_wait(&bars[B_SFREE + (js & 1)], ((js >> 1) - 1) & 1)) {
                             if (seg_left == 0) {
                                 int len, tiles;
                                 bool x = false;
@@ -275,31 +284,29 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                                 seg_left = (int)min((long long)tiles, ntile - js);
                                 seg_first = 1;
                             }
-                            if (!seg_first || mbar_try_wait(&bars[B_QFULL], seg & 1)) { u = a.R ? 1 : 2; moved = true; }
+                            if (!seg_first || mbar_test_wait(&bars[B_QFULL], seg & 1)) { u = a.R ? 1 : 2; moved = true; }
                         }
                     } else if (u == 1) {
                         const int s = (int)(js & 1);
-                        if (mbar_try_wait(&bars[B_SHFULL + s], (js >> 1) & 1)) {
+                        if (mbar_test_wait(&bars[B_SHFULL + s], (js >> 1) & 1)) {
                             tc_fence_after();
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                umma_ss(d, smem_desc(sbase + Y::Q + 8 * Y::QCHUNK + ks * 32, 16, 1024, SW_128B),
-                                        smem_desc(sbase + Y::SH + s * SH_SLOT + ks * 32, 16, 1024, SW_128B), id_s, ks > 0);
+                                umma_ss(d, desc64(q_lo + 8 * Y::QCHUNK / 16 + ks * 2, hi), desc64(sh_lo + s * (SH_SLOT / 16) + ks * 2, hi), id_s, ks > 0);
                             umma_commit(&bars[B_SHEMPTY + s]);
                             u = 2;
                             moved = true;
                         }
                     } else {
-                        const int c = u - 2;
-                        const long long i = js * 4 + c;
-                        const int s = (int)(i % Y::NSLOT);
-                        if (mbar_try_wait(&bars[B_FULL + s], (uint32_t)(i / Y::NSLOT) & 1)) {
+                        if (mbar_test_wait(&bars[B_FULL + ks_slot], ks_phase)) {
                             tc_fence_after();
+                            const uint32_t qc = q_lo + (u - 2) * (2 * Y::QCHUNK / 16), kc = k_lo + ks_slot * (SLOT / 16);
+                            const uint32_t more = (a.R || u > 2) ? 1u : 0u;
 #pragma unroll
                             for (int ks = 0; ks < 8; ++ks)
-                                umma_ss(d, smem_desc(sbase + Y::Q + (2 * c + (ks >> 2)) * Y::QCHUNK + (ks & 3) * 32, 16, 1024, SW_128B),
-                                        smem_desc(sbase + Y::RING + s * SLOT + (ks >> 2) * 8192 + (ks & 3) * 32, 16, 1024, SW_128B),
-                                        id_s, (a.R || c > 0 || ks > 0) ? 1 : 0);
+                                umma_ss(d, desc64(qc + (ks >> 2) * (Y::QCHUNK / 16) + (ks & 3) * 2, hi),
+                                        desc64(kc + (ks >> 2) * 512 + (ks & 3) * 2, hi), id_s, ks > 0 ? 1 : more);
+                            if (++ks_slot == Y::NSLOT) { ks_slot = 0; ks_phase ^= 1; }
                             moved = true;
                             if (++u == 6) {
                                 umma_commit(&bars[B_SFULL + (js & 1)]);
@@ -509,24 +516,48 @@ __global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a)
     const int n = a.meta[2 * share], last = a.meta[2 * share + 1];
     if (n < 0 || g * RG + r >= a.Tq * a.H) return;
     auto slot_of = [&](int s) { return ((size_t)(s * a.G + g) * 2 + (s == share ? 1 : 0)) * RG + r; };
-    float m = -INFINITY;
-    for (int s = share; s <= last; ++s) m = fmaxf(m, a.part_ml[slot_of(s) * 2]);
+    // the parts' factors first, all at once; then their values in turn
+    __shared__ float s_f[kLanes], s_red[2][4];
+    const int t = threadIdx.x, parts = last - share + 1;
+    float mine[2], ml[2], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        mine[i] = -INFINITY; ml[i] = 0.f;
+        if (t + 128 * i < parts) {
+            const float2 x = *reinterpret_cast<const float2 *>(a.part_ml + slot_of(share + t + 128 * i) * 2);
+            mine[i] = x.x; ml[i] = x.y;
+        }
+        m = fmaxf(m, mine[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((t & 31) == 0) s_red[0][t >> 5] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
     const float mu = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float f = exp2f(mine[i] - mu);
+        l += f * ml[i];
+        if (t + 128 * i < parts) s_f[t + 128 * i] = f;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if ((t & 31) == 0) s_red[1][t >> 5] = l;
+    __syncthreads();
+    l = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = share; s <= last; ++s) {
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + slot_of(s) * 2);
-        const float f = exp2f(ml.x - mu);
-        const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(s) * kLatentDim) + threadIdx.x);
-        l += f * ml.y;
+#pragma unroll 8
+    for (int s = 0; s < parts; ++s) {
+        const float f = s_f[s];
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(share + s) * kLatentDim) + t);
         o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const size_t row = (size_t)n * a.Tq * a.H + g * RG + r;
-    reinterpret_cast<uint2 *>(a.out + row * kLatentDim)[threadIdx.x] =
+    reinterpret_cast<uint2 *>(a.out + row * kLatentDim)[t] =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (threadIdx.x == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    if (t == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 bool al(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
