@@ -8,17 +8,21 @@
 // eighth of what the tensor cores could do meanwhile. So the kernel is built around the copies:
 //  - The queries of a sequence (Tq x H rows, in groups of at most 64) stay in shared memory, and the cache
 //    streams past them in tiles of 64 rows. One tile serves both products from the same shared memory: as
-//    K-major B operand of S = Q C^T and as MN-major A operand of O^T = C^T P^T. O^T (512 x rows, fp32) needs
+//    K-major A operand of S^T = C Q^T and as MN-major A operand of O^T = C^T P^T. O^T (512 x rows, fp32) needs
 //    4 x rows tensor-memory columns, where O itself would need all 512 for any number of rows.
-//  - S runs with M = 128; with 64 query rows or fewer the upper lanes read whatever lies behind the queries
-//    in shared memory and are never looked at.
+//  - The products are limited by what they read from shared memory (A 128 rows x 16 = 4 KB an instruction at
+//    128 bytes a cycle), which the copies' writes share: S^T with M = 64 reads 3 KB where S = Q C^T with
+//    M = 128 (rows behind the queries unused) reads 6 KB; it took 52 cycles an instruction, and the whole
+//    kernel 392 us where this takes @T1@ (256 sequences x 32 heads, 1.5 GB).
+//  - A thread of the softmax has one cache row and half of the query rows. It goes on with the running maxima
+//    it has and only checks, in the same barrier that the tile needs anyway, whether a score passed one of
+//    them by more than 2^8 (P stays below 2^8, l is fp32): maxima across threads, and the rescaling of O^T in
+//    tensor memory, are for the few tiles where one did.
 //  - The tiles of all sequences form one list, cut into equal shares, one per SM (`lanes`), whatever the
 //    sequences' lengths. A sequence that a cut runs through leaves partial results (unnormalised O, maximum,
 //    sum, fp32), which a second kernel joins in order of the shares: no atomics, the same bits each time.
 //    The groups of one sequence (more than 64 rows) take the same share at the same time on neighbouring
 //    SMs, so that one of them finds the other's tile in L2.
-//  - The running maximum moves only when a row's scores pass it by more than 2^8 (P then stays below 2^8,
-//    exact in range for bf16, and l is fp32): the rescaling of O^T in tensor memory becomes rare.
 // P is rounded to bf16 as the operand of the second product; sums and statistics are fp32.
 #include "latent.cuh"
 #include "sm100.cuh"
@@ -35,22 +39,21 @@ constexpr int W_LOAD = 8, W_MMA = 9;
 constexpr uint32_t SLOT = 16384;             // 64 cache rows x 128 latent channels: two 64-channel halves
 constexpr uint32_t SH_SLOT = 8192;           // 64 cache rows x the 64 shared channels
 
-// Shared memory for groups of RG query rows (16, 32 or 64): queries (9 chunks of 64 channels), P twice, the
-// shared key parts twice, and a ring of latent slots in what is left (a tile is four slots).
+// Shared memory for groups of RG query rows (32 or 64): queries (9 chunks of 64 channels), P^T twice (64 cache
+// rows of RG values), the shared key parts twice, and a ring of latent slots in what is left (a tile is four).
 template <int RG> struct Lay {
     static constexpr uint32_t Q = 0, QCHUNK = RG * 128;
-    static constexpr uint32_t P = 9 * QCHUNK, PBUF = RG * 128 < 1024 ? 1024 : RG * 128;
+    static constexpr uint32_t P = 9 * QCHUNK, PBUF = KT * RG * 2;
     static constexpr uint32_t SH = P + 2 * PBUF;
     static constexpr uint32_t RING = SH + 2 * SH_SLOT;
     static constexpr int NSLOT = RG == 64 ? 7 : 10;
-    static constexpr uint32_t MAXS = RING + NSLOT * SLOT;         // float [2][2][64]: by tile parity, each half's row maxima
-    static constexpr uint32_t LSUM = MAXS + 1024;                 // float [2][64]: each half's row sums
-    static constexpr uint32_t BAR = LSUM + 512;
+    static constexpr uint32_t RED = RING + NSLOT * SLOT;          // float [4][RG]: each quarter's maxima, then its sums
+    static constexpr uint32_t FAC = RED + 4 * RG * 4;             // float [RG]: factors of the columns of O^T
+    static constexpr uint32_t MAXS = FAC + RG * 4;                // float [RG]: running maxima at a segment's end
+    static constexpr uint32_t BAR = MAXS + RG * 4;
     static constexpr uint32_t TOTAL = BAR + 512 + 1024;           // with room to align the base
-    static_assert(TOTAL <= 232448, "shared memory");
-    static_assert(QCHUNK % 1024 == 0 && P % 1024 == 0, "swizzle atoms");
-    // the M = 128 product reads 128 rows from the start of each query chunk
-    static_assert(8 * QCHUNK + 128 * 128 <= MAXS, "queries' overread");
+    static_assert(TOTAL + 3072 <= 232448, "shared memory");
+    static_assert(QCHUNK % 1024 == 0 && P % 1024 == 0 && PBUF % 1024 == 0, "swizzle atoms");
 };
 
 struct DecodeArgs {
@@ -69,6 +72,23 @@ enum { B_QFULL, B_QEMPTY, B_SHFULL, B_SHEMPTY = B_SHFULL + 2, B_SFULL = B_SHEMPT
        B_PREADY = B_SFREE + 2, B_PVDONE = B_PREADY + 2, B_FULL = B_PVDONE + 2, B_EMPTY = B_FULL + 10, B_DRAIN = B_EMPTY + 10,
        N_BARS };
 static_assert(N_BARS * 8 + 64 <= 512, "barriers");
+
+__device__ __forceinline__ float warp_max(float x)
+{
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
+    return x;
+}
+
+// Barrier of `nthreads` threads that tells each whether any of them holds.
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t nthreads, bool mine)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+                 "barrier.cta.red.or.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(r) : "r"(id), "r"(nthreads), "r"((uint32_t)mine) : "memory");
+    return r != 0;
+}
 
 __device__ __forceinline__ int tiles_of(const DecodeArgs &a, int n, int *len_out, bool *bad)
 {
@@ -239,9 +259,10 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         // One thread runs both products as their operands arrive: scores of a tile slot by slot while its
         // copies land, the second product of the tile before as soon as its P is there.
         if (elect_one()) {
-            constexpr uint32_t id_s = idesc_bf16(128, KT, 0, 0), id_o = idesc_bf16(128, RG, 1, 0);
-            constexpr uint32_t hi = desc_hi(1024, SW_128B);
-            // K-major operands (queries, cache rows as keys, P) and the cache rows as MN-major values
+            constexpr uint32_t id_s = idesc_bf16(KT, RG, 0, 0), id_o = idesc_bf16(128, RG, 1, 1);
+            constexpr uint32_t hi = desc_hi(1024, SW_128B), hi_p = RG == 64 ? hi : desc_hi(512, SW_64B);
+            // K-major operands (cache rows as keys, queries), and MN-major ones: the cache rows as values, and P^T,
+            // whose RG values a row are one swizzle atom wide
             const uint32_t q_lo = desc_lo(sbase + Y::Q, 16), p_lo = desc_lo(sbase + Y::P, 16), sh_lo = desc_lo(sbase + Y::SH, 16);
             const uint32_t k_lo = desc_lo(sbase + Y::RING, 16), v_lo = desc_lo(sbase + Y::RING, 8192);
             const long long ntile = end - begin;
@@ -265,7 +286,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                         const uint32_t slot = v_lo + ps * (SLOT / 16);
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            umma_ss(TM_O + c * RG, desc64(slot + ks * 128, hi), desc64(pb + ks * 2, hi), id_o, ks > 0 ? 1 : more);
+                            umma_ss(TM_O + c * RG, desc64(slot + ks * 128, hi), desc64(pb + ks * (RG * 2), hi_p), id_o, ks > 0 ? 1 : more);
                         umma_commit(&bars[B_EMPTY + ps]);
                         if (++ps == Y::NSLOT) ps = 0;
                     }
@@ -292,7 +313,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                             tc_fence_after();
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                umma_ss(d, desc64(q_lo + 8 * Y::QCHUNK / 16 + ks * 2, hi), desc64(sh_lo + s * (SH_SLOT / 16) + ks * 2, hi), id_s, ks > 0);
+                                umma_ss(d, desc64(sh_lo + s * (SH_SLOT / 16) + ks * 2, hi), desc64(q_lo + 8 * Y::QCHUNK / 16 + ks * 2, hi), id_s, ks > 0);
                             umma_commit(&bars[B_SHEMPTY + s]);
                             u = 2;
                             moved = true;
@@ -304,8 +325,8 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                             const uint32_t more = (a.R || u > 2) ? 1u : 0u;
 #pragma unroll
                             for (int ks = 0; ks < 8; ++ks)
-                                umma_ss(d, desc64(qc + (ks >> 2) * (Y::QCHUNK / 16) + (ks & 3) * 2, hi),
-                                        desc64(kc + (ks >> 2) * 512 + (ks & 3) * 2, hi), id_s, ks > 0 ? 1 : more);
+                                umma_ss(d, desc64(kc + (ks >> 2) * 512 + (ks & 3) * 2, hi),
+                                        desc64(qc + (ks >> 2) * (Y::QCHUNK / 16) + (ks & 3) * 2, hi), id_s, ks > 0 ? 1 : more);
                             if (++ks_slot == Y::NSLOT) { ks_slot = 0; ks_phase ^= 1; }
                             moved = true;
                             if (++u == 6) {
@@ -329,15 +350,16 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         }
     } else {
         // ============================================================================ softmax
-        // Warp w reads tensor-memory lanes 32 (w % 4) ..: for S the query rows (warps with w % 4 < RG / 32),
-        // columns 32 (w / 4) .. of the tile; for O^T the latent channels of chunks 2 (w / 4) and 2 (w / 4) + 1.
+        // Warp w has the cache rows 16 (w % 4) .. of the tile, one for each of its first 16 lanes (where a product
+        // with M = 64 leaves them), and the query rows HP (w / 4) ..; of O^T the latent channels of chunks
+        // 2 (w / 4) and 2 (w / 4) + 1, all 128 lanes.
+        constexpr int HP = RG / 2;
+        constexpr float kNone = -1e30f, kOff = 1e30f;        // no score yet; a row that is none
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t lanes = (uint32_t)quad << 21;
-        const bool active = quad < (RG == 64 ? 2 : 1);
-        float *smax = reinterpret_cast<float *>(sm + Y::MAXS), *slsum = reinterpret_cast<float *>(sm + Y::LSUM);
-        const int row = quad * 32 + lane;                    // active warps: this thread's query row
-        const bool real = active && row < rows;
-        const int tq = real ? (g * RG + row) / a.H : 0;
+        const int key = quad * 16 + lane;                    // lanes below 16
+        float *red = reinterpret_cast<float *>(sm + Y::RED), *fac = reinterpret_cast<float *>(sm + Y::FAC);
+        float *mseg = reinterpret_cast<float *>(sm + Y::MAXS);
         long long j = 0;                                     // tile of this share
         int n = n0, off = off0;
         long long left = end - begin, pfx = s_prefix;        // pfx: tiles before sequence n
@@ -347,35 +369,36 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
             bool x = false;
             const int tiles = tiles_of(a, n, &len, &x), cnt = (int)min((long long)(tiles - off), left);
             if (cnt <= 0) { ++n; off = 0; continue; }
-            const int lim = real ? max(0, len - a.Tq + tq + 1) : 0;
-            // every warp keeps the running maxima of rows `lane` and `lane + 32` (log2 domain)
-            float m_lo = -INFINITY, m_hi = -INFINITY, lsum = 0.f;
+            float m[HP], lsum[HP];                           // running maxima (log2 domain), this thread's part of the sums
+#pragma unroll
+            for (int i = 0; i < HP; ++i) { m[i] = half * HP + i < rows ? kNone : kOff; lsum[i] = 0.f; }
             for (int t = off; t < off + cnt; ++t, ++j) {
                 const int buf = (int)(j & 1);
                 wait(B_SFULL + buf, (uint32_t)(j >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
-                float s[32];
-                if (active) {
-                    tmem_ld32_sync(tmem + lanes + buf * 64 + half * 32, s);
-                    tc_fence_before();
-                }
+                float s[HP];
+#pragma unroll
+                for (int q = 0; q < HP / 16; ++q)
+                    tmem_ld16_sync(tmem + lanes + buf * 64 + half * HP + q * 16, *reinterpret_cast<float (*)[16]>(s + q * 16));
+                tc_fence_before();
                 __syncwarp();
-                // every warp, so that none can still be waiting for this phase when the buffer's next one ends
                 if (lane == 0) mbar_arrive(&bars[B_SFREE + buf]);
-                float *mx_tile = smax + buf * 128;
-                if (active) {
-                    const int k0 = t * KT + half * 32;
-                    float mx = -INFINITY;
-                    if (k0 + 32 <= lim) {
+                const int k = t * KT + key;
+                if (lane >= 16) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) { s[i] *= a.scale_log2; mx = fmaxf(mx, s[i]); }
-                    } else {
+                    for (int i = 0; i < HP; ++i) s[i] = -INFINITY;
+                } else if (t * KT + KT > len - a.Tq + 1) {   // a tile whose last rows some query row does not see
+                    int h = (g * RG + half * HP) % a.H, lim = len - a.Tq + 1 + (g * RG + half * HP) / a.H;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) { s[i] = k0 + i < lim ? s[i] * a.scale_log2 : -INFINITY; mx = fmaxf(mx, s[i]); }
+                    for (int i = 0; i < HP; ++i) {
+                        if (k >= lim) s[i] = -INFINITY;
+                        if (++h == a.H) { h = 0; ++lim; }
                     }
-                    mx_tile[half * 64 + row] = mx;
                 }
+                float top = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < HP; ++i) top = fmaxf(top, s[i] * a.scale_log2 - m[i]);
                 // rows of the tile behind the sequence's end may hold anything: zeros, as values
                 const int valid = len - t * KT;
                 if (valid < KT) {
@@ -388,15 +411,23 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                     }
                     fence_proxy_async_smem();
                 }
-                named_bar_sync(1, NSOFT);
-                const float c_lo = fmaxf(mx_tile[lane], mx_tile[64 + lane]);
-                const float c_hi = RG == 64 ? fmaxf(mx_tile[32 + lane], mx_tile[96 + lane]) : -INFINITY;
-                const bool up = c_lo > m_lo + 8.f || c_hi > m_hi + 8.f;
-                if (__any_sync(0xffffffffu, up)) {           // the same outcome in all warps
-                    const float q_lo = fmaxf(m_lo, c_lo), q_hi = fmaxf(m_hi, c_hi);
-                    const float f_lo = q_lo == m_lo ? 1.f : exp2f(m_lo - q_lo), f_hi = q_hi == m_hi ? 1.f : exp2f(m_hi - q_hi);
-                    m_lo = q_lo; m_hi = q_hi;
-                    if (active) lsum *= (quad & 1) ? f_hi : f_lo;
+                if (bar_or(1, NSOFT, top > 8.f)) {           // the same outcome in all warps
+#pragma unroll
+                    for (int i = 0; i < HP; ++i) {
+                        const float mx = warp_max(s[i]);
+                        if (lane == 0) red[quad * RG + half * HP + i] = mx;
+                    }
+                    named_bar_sync(1, NSOFT);
+#pragma unroll
+                    for (int i = 0; i < HP; ++i) {
+                        const int r = half * HP + i;
+                        const float mx = fmaxf(fmaxf(red[r], red[RG + r]), fmaxf(red[2 * RG + r], red[3 * RG + r])) * a.scale_log2;
+                        const float up = fmaxf(m[i], mx), f = up == m[i] ? 1.f : ex2(m[i] - up);
+                        m[i] = up;
+                        lsum[i] *= f;
+                        if (quad == 0 && lane == 0) fac[r] = f;
+                    }
+                    named_bar_sync(1, NSOFT);
                     if (t > off) {
                         wait(B_PVDONE + (buf ^ 1), (uint32_t)((j - 1) >> 1) & 1);
                         __syncwarp();
@@ -409,8 +440,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                                 float o[16];
                                 tmem_ld16_sync(ad, o);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    o[i] *= __shfl_sync(0xffffffffu, q < 2 ? f_lo : f_hi, (q & 1) * 16 + i);
+                                for (int i = 0; i < 16; ++i) o[i] *= fac[q * 16 + i];
                                 tmem_st16(ad, o);
                             }
                         }
@@ -418,22 +448,23 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                         tc_fence_before();
                     }
                 }
-                if (active) {
-                    const float m = (quad & 1) ? m_hi : m_lo;
-                    const float mu = m == -INFINITY ? 0.f : m;
-                    // P's buffer was last read by the second product of tile j - 2
-                    if (j >= 2) { wait(B_PVDONE + buf, (uint32_t)((j >> 1) - 1) & 1); __syncwarp(); }
-                    unsigned char *pr = sm + Y::P + buf * Y::PBUF + row * 128;
+                // P's buffer was last read by the second product of tile j - 2
+                if (j >= 2) { wait(B_PVDONE + buf, (uint32_t)((j >> 1) - 1) & 1); __syncwarp(); }
+                if (lane < 16) {
+                    unsigned char *pr = sm + Y::P + buf * Y::PBUF;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < HP / 8; ++c) {
                         uint32_t w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float p0 = ex2(s[8 * c + 2 * i] - mu), p1 = ex2(s[8 * c + 2 * i + 1] - mu);
-                            lsum += p0 + p1;
+                            const int e = 8 * c + 2 * i;
+                            const float p0 = ex2(s[e] * a.scale_log2 - m[e]), p1 = ex2(s[e + 1] * a.scale_log2 - m[e + 1]);
+                            lsum[e] += p0;
+                            lsum[e + 1] += p1;
                             w[i] = pack_bf16x2(p0, p1);
                         }
-                        if (row < RG) *reinterpret_cast<uint4 *>(pr + (((half * 4 + c) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        const uint32_t at = RG == 64 ? sw128_offset(key, half * HP + 8 * c) : sw64_offset(key, half * HP + 8 * c);
+                        *reinterpret_cast<uint4 *>(pr + at) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     fence_proxy_async_smem();
                 }
@@ -441,18 +472,33 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                 if (lane == 0) mbar_arrive(&bars[B_PREADY + buf]);
             }
             // -------- the segment's results
-            if (active) slsum[half * 64 + row] = lsum;
+#pragma unroll
+            for (int i = 0; i < HP; ++i) {
+                float v = lane < 16 ? lsum[i] : 0.f;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (lane == 0) {
+                    red[quad * RG + half * HP + i] = v;
+                    if (quad == 0) mseg[half * HP + i] = m[i];
+                }
+            }
             const long long jl = j - 1;
             wait(B_PVDONE + (jl & 1), (uint32_t)(jl >> 1) & 1);
             __syncwarp();
             tc_fence_after();
             named_bar_sync(1, NSOFT);
-            const float l_lo = slsum[lane] + slsum[64 + lane], l_hi = RG == 64 ? slsum[32 + lane] + slsum[96 + lane] : 0.f;
             const bool whole = off == 0 && cnt == tiles;
-            const float i_lo = whole ? (l_lo > 0.f ? 1.f / l_lo : (l_lo == 0.f ? 0.f : l_lo)) : 1.f;
-            const float i_hi = whole ? (l_hi > 0.f ? 1.f / l_hi : (l_hi == 0.f ? 0.f : l_hi)) : 1.f;
             const size_t r0 = (size_t)n * a.Tq * a.H + g * RG;
             const size_t pslot = (size_t)blockIdx.x * 2 + (off == 0 ? 1 : 0);
+            if (tid < RG) {
+                const float l = (red[tid] + red[RG + tid]) + (red[2 * RG + tid] + red[3 * RG + tid]), mm = mseg[tid];
+                fac[tid] = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                if (tid < rows) {
+                    if (whole) a.lse[r0 + tid] = l == 0.f ? -INFINITY : (mm + log2f(l)) * 0.69314718055994531f;
+                    else *reinterpret_cast<float2 *>(a.part_ml + (pslot * RG + tid) * 2) = make_float2(l == 0.f ? -INFINITY : mm, l);
+                }
+            }
+            named_bar_sync(1, NSOFT);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int dim = (2 * half + c) * 128 + quad * 32 + lane;
@@ -462,23 +508,11 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                     tmem_ld16_sync(TM_O + lanes + (2 * half + c) * RG + q * 16, o);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float v = o[i] * __shfl_sync(0xffffffffu, q < 2 ? i_lo : i_hi, (q & 1) * 16 + i);
                         const int r = q * 16 + i;
                         if (r < rows) {
-                            if (whole) a.out[(r0 + r) * kLatentDim + dim] = __float2bfloat16_rn(v);
-                            else a.part[(pslot * RG + r) * kLatentDim + dim] = v;
+                            if (whole) a.out[(r0 + r) * kLatentDim + dim] = __float2bfloat16_rn(o[i] * fac[r]);
+                            else a.part[(pslot * RG + r) * kLatentDim + dim] = o[i];
                         }
-                    }
-                }
-            }
-            if (warp == 0) {
-#pragma unroll
-                for (int i = 0; i < (RG == 64 ? 2 : 1); ++i) {
-                    const int r = lane + 32 * i;
-                    const float m = i ? m_hi : m_lo, l = i ? l_hi : l_lo;
-                    if (r < rows) {
-                        if (whole) a.lse[r0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-                        else *reinterpret_cast<float2 *>(a.part_ml + (pslot * RG + r) * 2) = make_float2(m, l);
                     }
                 }
             }
@@ -568,7 +602,7 @@ struct Plan { int RG, G, L; size_t meta, errs, part, ml, total; };
 Plan plan_of(long long rows)
 {
     Plan p;
-    p.RG = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    p.RG = rows <= 32 ? 32 : 64;
     p.G = (int)((rows + p.RG - 1) / p.RG);
     p.L = p.G >= kLanes ? 1 : kLanes / p.G;
     size_t off = kStatusBytes;
@@ -650,7 +684,7 @@ kda_status_t kda_latent_decode_step(const void *q, const void *cache, const int3
     if (crows > 0 && (!bf16_rows_map(&tq, q, W, qrows, W, 64, pl.RG) || !bf16_rows_map(&tc, cache, W, crows, W, 64, a.box)))
         return KDA_ERR_CUDA;
     if (crows == 0) a.max_pages = 0;
-    const cudaError_t e = pl.RG == 16 ? launch<16>(a, tq, tc, st) : pl.RG == 32 ? launch<32>(a, tq, tc, st) : launch<64>(a, tq, tc, st);
+    const cudaError_t e = pl.RG == 32 ? launch<32>(a, tq, tc, st) : launch<64>(a, tq, tc, st);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
