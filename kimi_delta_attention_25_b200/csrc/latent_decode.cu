@@ -34,14 +34,15 @@ using namespace sm100;
 
 constexpr int KT = 64;                       // cache rows per tile
 constexpr int kLanes = 148;                  // shares of the list of tiles: one per SM of a B200
-constexpr int NSOFT = 256, NT = NSOFT + 64;  // softmax warps 0..7, loader 8, MMA issuer 9
-constexpr int W_LOAD = 8, W_MMA = 9;
+constexpr int HP = 16;                       // query rows of one softmax thread
 constexpr uint32_t SLOT = 16384;             // 64 cache rows x 128 latent channels: two 64-channel halves
 constexpr uint32_t SH_SLOT = 8192;           // 64 cache rows x the 64 shared channels
 
 // Shared memory for groups of RG query rows (32 or 64): queries (9 chunks of 64 channels), P^T twice (64 cache
 // rows of RG values), the shared key parts twice, and a ring of latent slots in what is left (a tile is four).
 template <int RG> struct Lay {
+    static constexpr int WG = RG / HP;                            // softmax warpgroups
+    static constexpr int NSOFT = 128 * WG, W_LOAD = 4 * WG, W_MMA = W_LOAD + 1, NT = NSOFT + 64;
     static constexpr uint32_t Q = 0, QCHUNK = RG * 128;
     static constexpr uint32_t P = 9 * QCHUNK, PBUF = KT * RG * 2;
     static constexpr uint32_t SH = P + 2 * PBUF;
@@ -52,7 +53,7 @@ template <int RG> struct Lay {
     static constexpr uint32_t MAXS = FAC + RG * 4;                // float [RG]: running maxima at a segment's end
     static constexpr uint32_t BAR = MAXS + RG * 4;
     static constexpr uint32_t TOTAL = BAR + 512 + 1024;           // with room to align the base
-    static_assert(TOTAL + 3072 <= 232448, "shared memory");
+    static_assert(TOTAL + 1024 <= 232448, "shared memory");
     static_assert(QCHUNK % 1024 == 0 && P % 1024 == 0 && PBUF % 1024 == 0, "swizzle atoms");
 };
 
@@ -75,9 +76,9 @@ static_assert(N_BARS * 8 + 64 <= 512, "barriers");
 
 __device__ __forceinline__ float warp_max(float x)
 {
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, m));
-    return x;
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
 }
 
 // Barrier of `nthreads` threads that tells each whether any of them holds.
@@ -99,10 +100,11 @@ __device__ __forceinline__ int tiles_of(const DecodeArgs &a, int n, int *len_out
 }
 
 template <int RG>
-__global__ void __launch_bounds__(NT, 1)
+__global__ void __launch_bounds__(Lay<RG>::NT, 1)
 latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c)
 {
     using Y = Lay<RG>;
+    constexpr int NT = Y::NT, NSOFT = Y::NSOFT, W_LOAD = Y::W_LOAD, W_MMA = Y::W_MMA;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(sm);
@@ -110,7 +112,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
     const int share = blockIdx.x / a.G, g = blockIdx.x % a.G;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Y::BAR);
     volatile int *ctl = reinterpret_cast<volatile int *>(bars + N_BARS);   // [0] tmem, [1] abort, [2] error, [3] n0, [4] off0
-    __shared__ long long s_scan[NT], s_prefix;
+    __shared__ long long s_warp[NT / 32], s_prefix;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
@@ -121,8 +123,8 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
             mbar_init(&bars[B_SHFULL + i], 1);
             mbar_init(&bars[B_SHEMPTY + i], 1);
             mbar_init(&bars[B_SFULL + i], 1);
-            mbar_init(&bars[B_SFREE + i], 8);
-            mbar_init(&bars[B_PREADY + i], 8);
+            mbar_init(&bars[B_SFREE + i], 4 * Y::WG);
+            mbar_init(&bars[B_PREADY + i], 4 * Y::WG);
             mbar_init(&bars[B_PVDONE + i], 1);
         }
         for (int i = 0; i < Y::NSLOT; ++i) { mbar_init(&bars[B_FULL + i], 1); mbar_init(&bars[B_EMPTY + i], 1); }
@@ -137,20 +139,25 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
     bool bad = false;
     long long mine = 0;
     for (int n = n_lo; n < n_hi; ++n) { int len; mine += tiles_of(a, n, &len, &bad); }
-    s_scan[tid] = mine;
-    __syncthreads();
-    for (int o = 1; o < NT; o <<= 1) {
-        const long long v = tid >= o ? s_scan[tid - o] : 0;
-        __syncthreads();
-        s_scan[tid] += v;
-        __syncthreads();
+    long long upto = mine;                                     // inclusive sums: within the warp, then over the warps
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
     }
-    const long long total = s_scan[NT - 1];
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        if (w < warp) upto += s_warp[w];
+        total += s_warp[w];
+    }
     // shares that get tiles: with fewer tiles than shares one each, so that no share inside a cut sequence is empty
     const int used = (int)min((long long)a.L, total);
     const long long begin = share < used ? total * share / used : 0, end = share < used ? total * (share + 1) / used : 0;
     {
-        long long at = s_scan[tid] - mine;
+        long long at = upto - mine;
         if (begin >= at && begin < at + mine && begin < end)
             for (int n = n_lo; n < n_hi; ++n) {
                 int len;
@@ -201,13 +208,6 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
             bool x = false;
             const int tiles = tiles_of(a, n, &len, &x), cnt = (int)min((long long)(tiles - off), left);
             if (cnt <= 0) { ++n; off = 0; continue; }
-            // the sequence's queries, once the last segment's scores are done
-            if (seg > 0) ok = wait(B_QEMPTY, (seg - 1) & 1);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive_expect_tx(&bars[B_QFULL], chunks * Y::QCHUNK);
-            __syncwarp();
-            if (lane < chunks) tma_load_2d(sm + Y::Q + lane * Y::QCHUNK, &tm_q, &bars[B_QFULL], lane * 64, n * a.Tq * a.H + g * RG);
             // row coordinate of this lane's box in tile t; behind the last row, or on a page that is not there, the
             // copy starts behind the cache and reads zeros
             // (the table's entry is read a tile ahead and looked at when its turn comes)
@@ -243,6 +243,16 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                     if (half < 2) tma_load_2d(sm + Y::RING + s * SLOT + half * 8192 + b * a.box * 128, &tm_c, &bars[B_FULL + s], c * 128 + half * 64, c1);
                     slots_used = i + 1;
                     if (++slot_next == Y::NSLOT) { slot_next = 0; slot_phase ^= 1; }
+                    if (c == 1 && t == off) {
+                        // the sequence's queries, once the last segment's scores are done (not in front of the cache
+                        // rows, which need not wait; not behind them all, as the ring may be too short for that)
+                        if (seg > 0) ok = wait(B_QEMPTY, (seg - 1) & 1);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(&bars[B_QFULL], chunks * Y::QCHUNK);
+                        __syncwarp();
+                        if (lane < chunks) tma_load_2d(sm + Y::Q + lane * Y::QCHUNK, &tm_q, &bars[B_QFULL], lane * 64, n * a.Tq * a.H + g * RG);
+                    }
                 }
             }
             ++seg; left -= cnt; ++n; off = 0;
@@ -256,106 +266,101 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         }
     } else if (warp == W_MMA) {
         // ======================================================================== MMA issuer
-        // One thread runs both products as their operands arrive: scores of a tile slot by slot while its
-        // copies land, the second product of the tile before as soon as its P is there.
-        if (elect_one()) {
-            constexpr uint32_t id_s = idesc_bf16(KT, RG, 0, 0), id_o = idesc_bf16(128, RG, 1, 1);
-            constexpr uint32_t hi = desc_hi(1024, SW_128B), hi_p = RG == 64 ? hi : desc_hi(512, SW_64B);
-            // K-major operands (cache rows as keys, queries), and MN-major ones: the cache rows as values, and P^T,
-            // whose RG values a row are one swizzle atom wide
-            const uint32_t q_lo = desc_lo(sbase + Y::Q, 16), p_lo = desc_lo(sbase + Y::P, 16), sh_lo = desc_lo(sbase + Y::SH, 16);
-            const uint32_t k_lo = desc_lo(sbase + Y::RING, 16), v_lo = desc_lo(sbase + Y::RING, 8192);
-            const long long ntile = end - begin;
-            int n = n0, off = off0, seg = 0, seg_left = 0, seg_first = 1;
-            long long js = 0, jp = 0;          // next tile of the scores, of the second product
-            int u = 0;                         // next operand of the scores' tile: 0 checks, 1 shared part, 2..5 latent slots
-            // first tiles of segments, for the second product's accumulate flag (by tile modulo 8: at most three are pending)
-            uint32_t first_bits = 0;
-            int ps = 0, ks_slot = 0;           // ring slots of the second product and of the scores
-            uint32_t ks_phase = 0;
-            long long t0 = clock64();
-            bool ok = true;
-            while (jp < ntile) {
-                bool moved = false;
-                if (jp < js && mbar_test_wait(&bars[B_PREADY + (jp & 1)], (jp >> 1) & 1)) {
-                    tc_fence_after();
-                    const uint32_t more = ((first_bits >> (jp & 7)) & 1) ^ 1u;
-                    const uint32_t pb = p_lo + (uint32_t)(jp & 1) * (Y::PBUF / 16);
+        // Scores of tile jt and the second product of the tile before, in a fixed order: half of the scores, the
+        // second product (whose P is ready by then, and whose end frees ring slots), the other half. The whole
+        // warp runs the loop and one thread issues, so that slots and addresses stay warp-uniform: operands of a
+        // product come from uniform registers, and moving them there one by one took 63 cycles a product.
+        const bool el = elect_one();
+        constexpr uint32_t id_s = idesc_bf16(KT, RG, 0, 0), id_o = idesc_bf16(128, RG, 1, 1);
+        constexpr uint32_t hi = desc_hi(1024, SW_128B), hi_p = RG == 64 ? hi : desc_hi(512, SW_64B);
+        // K-major operands (cache rows as keys, queries), and MN-major ones: the cache rows as values, and P^T,
+        // whose RG values a row are one swizzle atom wide
+        const uint32_t q_lo = desc_lo(sbase + Y::Q, 16), p_lo = desc_lo(sbase + Y::P, 16), sh_lo = desc_lo(sbase + Y::SH, 16);
+        const uint32_t k_lo = desc_lo(sbase + Y::RING, 16), v_lo = desc_lo(sbase + Y::RING, 8192);
+        const int ntile = __reduce_max_sync(0xffffffffu, (int)(end - begin));
+        const uint32_t has_r = a.R != 0;
+        int n = n0, off = off0, seg = 0, seg_left = 0;
+        int sslot = 0, pslot = 0;
+        uint32_t sphase = 0, first_s = 0, first_p = 0;
+        auto scores = [&](int c0, int c1, uint32_t d) {
+            for (int c = c0; c < c1; ++c) {
+                wait(B_FULL + sslot, sphase);
+                tc_fence_after();
+                if (el) {
+                    const uint32_t qc = q_lo + c * (2 * Y::QCHUNK / 16), kc = k_lo + sslot * (SLOT / 16);
+                    const uint32_t more = has_r | (c > 0 ? 1u : 0u);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t slot = v_lo + ps * (SLOT / 16);
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_ss(d, desc64(kc + (ks >> 2) * 512 + (ks & 3) * 2, hi),
+                                desc64(qc + (ks >> 2) * (Y::QCHUNK / 16) + (ks & 3) * 2, hi), id_s, ks > 0 ? 1 : more);
+                }
+                if (++sslot == Y::NSLOT) { sslot = 0; sphase ^= 1; }
+            }
+        };
+        for (int jt = 0; jt <= ntile; ++jt) {
+            const uint32_t d = tmem + (uint32_t)(jt & 1) * 64;
+            if (jt < ntile) {
+                if (jt >= 2) wait(B_SFREE + (jt & 1), (uint32_t)((jt >> 1) - 1) & 1);
+                first_s = 0;
+                if (seg_left == 0) {
+                    int len, tiles;
+                    bool x = false;
+                    while ((tiles = tiles_of(a, n, &len, &x) - off) <= 0) { ++n; off = 0; }
+                    seg_left = __reduce_max_sync(0xffffffffu, min(tiles, ntile - jt));
+                    wait(B_QFULL, seg & 1);
+                    first_s = 1;
+                }
+                if (has_r) {
+                    const int sh = jt & 1;
+                    wait(B_SHFULL + sh, (uint32_t)(jt >> 1) & 1);
+                    tc_fence_after();
+                    if (el) {
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            umma_ss(TM_O + c * RG, desc64(slot + ks * 128, hi), desc64(pb + ks * (RG * 2), hi_p), id_o, ks > 0 ? 1 : more);
-                        umma_commit(&bars[B_EMPTY + ps]);
-                        if (++ps == Y::NSLOT) ps = 0;
-                    }
-                    umma_commit(&bars[B_PVDONE + (jp & 1)]);
-                    ++jp;
-                    moved = true;
-                } else if (js < ntile) {
-                    const uint32_t d = tmem + (uint32_t)(js & 1) * 64;
-                    if (u == 0) {
-                        // the buffer of S is free, and at a segment's start its queries are there
-                        if (js < 2 || mbar_test_wait(&bars[B_SFREE + (js & 1)], ((js >> 1) - 1) & 1)) {
-                            if (seg_left == 0) {
-                                int len, tiles;
-                                bool x = false;
-                                while ((tiles = tiles_of(a, n, &len, &x) - off) <= 0) { ++n; off = 0; }
-                                seg_left = (int)min((long long)tiles, ntile - js);
-                                seg_first = 1;
-                            }
-                            if (!seg_first || mbar_test_wait(&bars[B_QFULL], seg & 1)) { u = a.R ? 1 : 2; moved = true; }
-                        }
-                    } else if (u == 1) {
-                        const int s = (int)(js & 1);
-                        if (mbar_test_wait(&bars[B_SHFULL + s], (js >> 1) & 1)) {
-                            tc_fence_after();
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                umma_ss(d, desc64(sh_lo + s * (SH_SLOT / 16) + ks * 2, hi), desc64(q_lo + 8 * Y::QCHUNK / 16 + ks * 2, hi), id_s, ks > 0);
-                            umma_commit(&bars[B_SHEMPTY + s]);
-                            u = 2;
-                            moved = true;
-                        }
-                    } else {
-                        if (mbar_test_wait(&bars[B_FULL + ks_slot], ks_phase)) {
-                            tc_fence_after();
-                            const uint32_t qc = q_lo + (u - 2) * (2 * Y::QCHUNK / 16), kc = k_lo + ks_slot * (SLOT / 16);
-                            const uint32_t more = (a.R || u > 2) ? 1u : 0u;
-#pragma unroll
-                            for (int ks = 0; ks < 8; ++ks)
-                                umma_ss(d, desc64(kc + (ks >> 2) * 512 + (ks & 3) * 2, hi),
-                                        desc64(qc + (ks >> 2) * (Y::QCHUNK / 16) + (ks & 3) * 2, hi), id_s, ks > 0 ? 1 : more);
-                            if (++ks_slot == Y::NSLOT) { ks_slot = 0; ks_phase ^= 1; }
-                            moved = true;
-                            if (++u == 6) {
-                                umma_commit(&bars[B_SFULL + (js & 1)]);
-                                first_bits = (first_bits & ~(1u << (js & 7))) | ((uint32_t)seg_first << (js & 7));
-                                seg_first = 0;
-                                if (--seg_left == 0) { umma_commit(&bars[B_QEMPTY]); ++seg; ++n; off = 0; }
-                                u = 0;
-                                ++js;
-                            }
-                        }
+                            umma_ss(d, desc64(sh_lo + sh * (SH_SLOT / 16) + ks * 2, hi),
+                                    desc64(q_lo + 8 * Y::QCHUNK / 16 + ks * 2, hi), id_s, ks > 0);
+                        umma_commit(&bars[B_SHEMPTY + sh]);
                     }
                 }
-                if (moved) { t0 = clock64(); continue; }
-                if (*abort_flag) { ok = false; break; }
-                if (clock64() - t0 > 2000000000LL) { *abort_flag = 1; ctl[2] = KDA_ERR_TIMEOUT; ok = false; break; }
+                scores(0, 2, d);
             }
-            (void)ok;
+            if (jt > 0) {
+                const int pb = (jt - 1) & 1;
+                wait(B_PREADY + pb, (uint32_t)((jt - 1) >> 1) & 1);
+                tc_fence_after();
+                const uint32_t more = first_p ^ 1u, pd = p_lo + pb * (Y::PBUF / 16);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (el) {
+                        const uint32_t vc = v_lo + pslot * (SLOT / 16);
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_ss(TM_O + c * RG, desc64(vc + ks * 128, hi), desc64(pd + ks * (RG * 2), hi_p), id_o, ks > 0 ? 1 : more);
+                        umma_commit(&bars[B_EMPTY + pslot]);
+                    }
+                    if (++pslot == Y::NSLOT) pslot = 0;
+                }
+                if (el) umma_commit(&bars[B_PVDONE + pb]);
+            }
+            if (jt < ntile) {
+                scores(2, 4, d);
+                if (el) umma_commit(&bars[B_SFULL + (jt & 1)]);
+                if (--seg_left == 0) { if (el) umma_commit(&bars[B_QEMPTY]); ++seg; ++n; off = 0; }
+            }
+            first_p = first_s;
+            if (*abort_flag) break;
+        }
+        if (el) {
             umma_commit(&bars[B_DRAIN]);
             if (!mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) ctl[2] = KDA_ERR_TIMEOUT;
         }
     } else {
         // ============================================================================ softmax
         // Warp w has the cache rows 16 (w % 4) .. of the tile, one for each of its first 16 lanes (where a product
-        // with M = 64 leaves them), and the query rows HP (w / 4) ..; of O^T the latent channels of chunks
-        // 2 (w / 4) and 2 (w / 4) + 1, all 128 lanes.
-        constexpr int HP = RG / 2;
+        // with M = 64 leaves them), and the query rows 16 (w / 4) ..; of O^T every (RG / 16)-th 128-channel chunk
+        // from w / 4 on, all 128 lanes.
         constexpr float kNone = -1e30f, kOff = 1e30f;        // no score yet; a row that is none
-        const int quad = warp & 3, half = warp >> 2;
+        const int quad = warp & 3, grp = warp >> 2;
         const uint32_t lanes = (uint32_t)quad << 21;
         const int key = quad * 16 + lane;                    // lanes below 16
         float *red = reinterpret_cast<float *>(sm + Y::RED), *fac = reinterpret_cast<float *>(sm + Y::FAC);
@@ -371,16 +376,14 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
             if (cnt <= 0) { ++n; off = 0; continue; }
             float m[HP], lsum[HP];                           // running maxima (log2 domain), this thread's part of the sums
 #pragma unroll
-            for (int i = 0; i < HP; ++i) { m[i] = half * HP + i < rows ? kNone : kOff; lsum[i] = 0.f; }
+            for (int i = 0; i < HP; ++i) { m[i] = grp * HP + i < rows ? kNone : kOff; lsum[i] = 0.f; }
             for (int t = off; t < off + cnt; ++t, ++j) {
                 const int buf = (int)(j & 1);
                 wait(B_SFULL + buf, (uint32_t)(j >> 1) & 1);
                 __syncwarp();
                 tc_fence_after();
                 float s[HP];
-#pragma unroll
-                for (int q = 0; q < HP / 16; ++q)
-                    tmem_ld16_sync(tmem + lanes + buf * 64 + half * HP + q * 16, *reinterpret_cast<float (*)[16]>(s + q * 16));
+                tmem_ld16_sync(tmem + lanes + buf * 64 + grp * HP, s);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[B_SFREE + buf]);
@@ -389,7 +392,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
 #pragma unroll
                     for (int i = 0; i < HP; ++i) s[i] = -INFINITY;
                 } else if (t * KT + KT > len - a.Tq + 1) {   // a tile whose last rows some query row does not see
-                    int h = (g * RG + half * HP) % a.H, lim = len - a.Tq + 1 + (g * RG + half * HP) / a.H;
+                    int h = (g * RG + grp * HP) % a.H, lim = len - a.Tq + 1 + (g * RG + grp * HP) / a.H;
 #pragma unroll
                     for (int i = 0; i < HP; ++i) {
                         if (k >= lim) s[i] = -INFINITY;
@@ -415,12 +418,12 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
 #pragma unroll
                     for (int i = 0; i < HP; ++i) {
                         const float mx = warp_max(s[i]);
-                        if (lane == 0) red[quad * RG + half * HP + i] = mx;
+                        if (lane == 0) red[quad * RG + grp * HP + i] = mx;
                     }
                     named_bar_sync(1, NSOFT);
 #pragma unroll
                     for (int i = 0; i < HP; ++i) {
-                        const int r = half * HP + i;
+                        const int r = grp * HP + i;
                         const float mx = fmaxf(fmaxf(red[r], red[RG + r]), fmaxf(red[2 * RG + r], red[3 * RG + r])) * a.scale_log2;
                         const float up = fmaxf(m[i], mx), f = up == m[i] ? 1.f : ex2(m[i] - up);
                         m[i] = up;
@@ -432,11 +435,11 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                         wait(B_PVDONE + (buf ^ 1), (uint32_t)((j - 1) >> 1) & 1);
                         __syncwarp();
                         tc_fence_after();
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-#pragma unroll
+#pragma unroll 1
+                        for (int c = grp; c < 4; c += Y::WG) {
+#pragma unroll 1
                             for (int q = 0; q < RG / 16; ++q) {
-                                const uint32_t ad = TM_O + lanes + (2 * half + c) * RG + q * 16;
+                                const uint32_t ad = TM_O + lanes + c * RG + q * 16;
                                 float o[16];
                                 tmem_ld16_sync(ad, o);
 #pragma unroll
@@ -463,7 +466,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                             lsum[e + 1] += p1;
                             w[i] = pack_bf16x2(p0, p1);
                         }
-                        const uint32_t at = RG == 64 ? sw128_offset(key, half * HP + 8 * c) : sw64_offset(key, half * HP + 8 * c);
+                        const uint32_t at = RG == 64 ? sw128_offset(key, grp * HP + 8 * c) : sw64_offset(key, grp * HP + 8 * c);
                         *reinterpret_cast<uint4 *>(pr + at) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     fence_proxy_async_smem();
@@ -478,8 +481,8 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
                 if (lane == 0) {
-                    red[quad * RG + half * HP + i] = v;
-                    if (quad == 0) mseg[half * HP + i] = m[i];
+                    red[quad * RG + grp * HP + i] = v;
+                    if (quad == 0) mseg[grp * HP + i] = m[i];
                 }
             }
             const long long jl = j - 1;
@@ -499,13 +502,14 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                 }
             }
             named_bar_sync(1, NSOFT);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int dim = (2 * half + c) * 128 + quad * 32 + lane;
-#pragma unroll
+#pragma unroll 1
+            for (int c = grp; c < 4; c += Y::WG) {
+                const int dim = c * 128 + quad * 32 + lane;
+#pragma unroll 1
                 for (int q = 0; q < RG / 16; ++q) {
+                    if (q * 16 >= rows) break;
                     float o[16];
-                    tmem_ld16_sync(TM_O + lanes + (2 * half + c) * RG + q * 16, o);
+                    tmem_ld16_sync(TM_O + lanes + c * RG + q * 16, o);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int r = q * 16 + i;
@@ -533,65 +537,121 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
     if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
-// Joins the partial results of each sequence that a cut runs through: block (share, group) x row, for the
-// sequence whose first part lies at the end of that share. The first block also gathers the blocks' errors
-// into the status word.
+// Joins the partial results of each sequence that a cut runs through. Block (cut, rows of a group, quarter of
+// the channels) with `rpb` rows. A sequence with many parts takes the whole block to a row and quarter, each warp
+// adding every fourth part; one with few parts takes a warp to a row, all of its channels, in the blocks of the
+// first quarter. The sums are added in a fixed order. The first block also gathers the blocks' errors into the
+// status word.
+constexpr int kManyParts = 8;
 template <int RG>
-__global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a)
+__global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int share = blockIdx.x / a.G, g = blockIdx.x % a.G, r = blockIdx.y;
-    if (blockIdx.x == 0 && r == 0) {
+    const int cut = blockIdx.x / a.G, g = blockIdx.x % a.G, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
         int err = 0;
-        for (int i = threadIdx.x; i < a.L * a.G; i += 128) err = max(err, a.errs[i]);
+        for (int i = t; i < a.L * a.G; i += 128) err = max(err, a.errs[i]);
         err = __syncthreads_or(err == KDA_ERR_TIMEOUT) ? KDA_ERR_TIMEOUT : (__syncthreads_or(err) ? KDA_ERR_INVALID_ARG : 0);
-        if (threadIdx.x == 0) *a.status = err;
+        if (t == 0) *a.status = err;
     }
-    const int n = a.meta[2 * share], last = a.meta[2 * share + 1];
-    if (n < 0 || g * RG + r >= a.Tq * a.H) return;
-    auto slot_of = [&](int s) { return ((size_t)(s * a.G + g) * 2 + (s == share ? 1 : 0)) * RG + r; };
-    // the parts' factors first, all at once; then their values in turn
-    __shared__ float s_f[kLanes], s_red[2][4];
-    const int t = threadIdx.x, parts = last - share + 1;
-    float mine[2], ml[2], m = -INFINITY, l = 0.f;
+    // the share at whose end the cut-th cut sequence begins
+    __shared__ int s_cut[4], s_found;
+    __shared__ float4 s_o[4][32];
+    int before = 0, share = -1;
+    if (t == 0) s_found = -1;
+    for (int base = 0; base < a.L; base += 128) {
+        const int i = base + t;
+        const bool is = i < a.L && a.meta[2 * i] >= 0;
+        const uint32_t ball = __ballot_sync(0xffffffffu, is);
+        if (lane == 0) s_cut[warp] = __popc(ball);
+        __syncthreads();
+        int at = before + __popc(ball & ((1u << lane) - 1));
+        for (int w = 0; w < 4; ++w) { if (w < warp) at += s_cut[w]; before += s_cut[w]; }
+        if (is && at == cut) s_found = i;
+        __syncthreads();
+    }
+    share = s_found;
+    if (share < 0) return;
+    const int n = a.meta[2 * share], last = a.meta[2 * share + 1], parts = last - share + 1;
+    const bool many = parts > kManyParts;
+    if (!many && blockIdx.z > 0) return;
+    auto slot_of = [&](int s, int r) { return ((size_t)((share + s) * a.G + g) * 2 + (s == 0 ? 1 : 0)) * RG + r; };
+    const int r_end = min(min(RG, a.Tq * a.H - g * RG), ((int)blockIdx.y + 1) * rpb);
+    const size_t row0 = (size_t)n * a.Tq * a.H + g * RG;
+    if (!many) {
+        for (int r = blockIdx.y * rpb + warp; r < r_end; r += 4) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < parts) ml = *reinterpret_cast<const float2 *>(a.part_ml + slot_of(lane, r) * 2);
+            const float m = warp_max(ml.x), f = ex2(ml.x - (m == -INFINITY ? 0.f : m));
+            float l = f * ml.y;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        mine[i] = -INFINITY; ml[i] = 0.f;
-        if (t + 128 * i < parts) {
-            const float2 x = *reinterpret_cast<const float2 *>(a.part_ml + slot_of(share + t + 128 * i) * 2);
-            mine[i] = x.x; ml[i] = x.y;
+            for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            l = __shfl_sync(0xffffffffu, l, 0);
+            float4 o[4] = {};
+#pragma unroll 2
+            for (int s = 0; s < parts; ++s) {
+                const float fs = __shfl_sync(0xffffffffu, f, s);
+                const float4 *src = reinterpret_cast<const float4 *>(a.part + slot_of(s, r) * kLatentDim) + lane;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float4 x = __ldcs(src + 32 * c);
+                    o[c].x += fs * x.x; o[c].y += fs * x.y; o[c].z += fs * x.z; o[c].w += fs * x.w;
+                }
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                reinterpret_cast<uint2 *>(a.out + (row0 + r) * kLatentDim)[32 * c + lane] =
+                    make_uint2(pack_bf16x2(o[c].x * inv, o[c].y * inv), pack_bf16x2(o[c].z * inv, o[c].w * inv));
+            if (lane == 0) a.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
         }
-        m = fmaxf(m, mine[i]);
+        return;
     }
+    __shared__ float s_f[kLanes], s_red[2][4];
+    for (int r = blockIdx.y * rpb; r < r_end; ++r) {
+        float2 ml[2];
+        float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((t & 31) == 0) s_red[0][t >> 5] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
-    const float mu = m == -INFINITY ? 0.f : m;
+        for (int i = 0; i < 2; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (t + 128 * i < parts) ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + slot_of(t + 128 * i, r) * 2);
+            m = fmaxf(m, ml[i].x);
+        }
+        m = warp_max(m);
+        if (lane == 0) s_red[0][warp] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float f = exp2f(mine[i] - mu);
-        l += f * ml[i];
-        if (t + 128 * i < parts) s_f[t + 128 * i] = f;
-    }
+        for (int i = 0; i < 2; ++i) {
+            const float f = ex2(ml[i].x - (m == -INFINITY ? 0.f : m));
+            l += f * ml[i].y;
+            if (t + 128 * i < parts) s_f[t + 128 * i] = f;
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if ((t & 31) == 0) s_red[1][t >> 5] = l;
-    __syncthreads();
-    l = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) s_red[1][warp] = l;
+        __syncthreads();
+        l = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
+        const int col = blockIdx.z * 32 + lane;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int s = 0; s < parts; ++s) {
-        const float f = s_f[s];
-        const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(share + s) * kLatentDim) + t);
-        o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+        for (int s = warp; s < parts; s += 4) {
+            const float f = s_f[s];
+            const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(s, r) * kLatentDim) + col);
+            o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+        }
+        s_o[warp][lane] = o;
+        __syncthreads();
+        if (warp == 0) {
+#pragma unroll
+            for (int w = 1; w < 4; ++w) { const float4 x = s_o[w][lane]; o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w; }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            reinterpret_cast<uint2 *>(a.out + (row0 + r) * kLatentDim)[col] =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            if (col == 0) a.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        }
+        __syncthreads();
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const size_t row = (size_t)n * a.Tq * a.H + g * RG + r;
-    reinterpret_cast<uint2 *>(a.out + row * kLatentDim)[t] =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (t == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 bool al(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
@@ -620,19 +680,21 @@ cudaError_t launch(const DecodeArgs &a, const CUtensorMap &tq, const CUtensorMap
     auto kern = latent_decode_kernel<RG>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<RG>::TOTAL);
     if (e != cudaSuccess) return e;
-    kern<<<a.L * a.G, NT, Lay<RG>::TOTAL, st>>>(a, tq, tc);
+    kern<<<a.L * a.G, Lay<RG>::NT, Lay<RG>::TOTAL, st>>>(a, tq, tc);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // the join's blocks may be scheduled while the last shares finish; they wait for the whole first kernel
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.L * a.G, RG < a.Tq * a.H ? RG : a.Tq * a.H);
+    // at most one cut a share and one a sequence; with few of them a block per row, else four rows to a block
+    const int cuts = a.N < a.L ? a.N : a.L, rows = RG < a.Tq * a.H ? RG : a.Tq * a.H, rpb = cuts * a.G <= 8 ? 1 : 4;
+    cfg.gridDim = dim3(cuts * a.G, (rows + rpb - 1) / rpb, 4);
     cfg.blockDim = dim3(128);
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_decode_join<RG>, a);
+    return cudaLaunchKernelEx(&cfg, latent_decode_join<RG>, a, rpb);
 }
 
 }  // namespace
