@@ -180,7 +180,7 @@ bool token_rows_map(CUtensorMap *m, const void *base, CUtensorMapDataType dt, ui
 
 // Tensor maps of bf16 rows for tiles of box_rows rows by box_cols (64: the 128-byte swizzle) columns:
 // [rows][cols] with a row stride (2 coordinates: column, row), and [rows][heads][cols] with row and head
-// strides (heads > 1: 3 coordinates: column, row, head). Strides in elements.
+// strides (3 coordinates: column, row, head). Strides in elements.
 bool bf16_rows_map(CUtensorMap *m, const void *base, long long cols, long long rows, long long row_stride,
                    uint32_t box_cols, uint32_t box_rows);
 bool bf16_heads_map(CUtensorMap *m, const void *base, long long cols, long long heads, long long rows,

@@ -3,47 +3,347 @@
 // channels, or none):  s_ij = scale (q_i[:128] . k_j + q_i[128:] . r_j),  o_i = sum_j softmax_j(s_ij) v_j.
 // Packed sequences with their own numbers of queries and keys; with `causal` query i of Lq sees the keys
 // up to i + Lk - Lq.
+//
+// The tensor cores bound it: 2 (192 + 128) flops per visible pair of tokens and head, where a score's
+// exponential costs one of 16 a cycle: 1024 cycles per 128 x 128 tile beside 1340 of products. The kernel
+// therefore works on two query tiles of 128 rows at once, one CTA per SM: while the tensor cores run one
+// tile's products (S = Q K^T, then O += P V), the other tile's warpgroup computes its P.
+//  - One row of a tile is one thread: the running maximum and sum need no exchange. S comes from tensor
+//    memory into registers, P goes back over S's columns in bf16 and is the A operand of the second
+//    product from there; O stays in tensor memory for the whole row of tiles (2 x (128 + 128) columns).
+//  - The maximum moves only when a row's scores pass it by more than 2^8 (P stays below 2^8, l is fp32), so
+//    that O is rarely rescaled; the same threads do it.
+//  - P is handed over in two halves, and the second product starts on the first while the second's
+//    exponentials are being taken.
+//  - Keys and values stream through a ring of eight 16 KB units (128 rows x 64 channels), each freed by the
+//    product that used it last; the shared key part is the third unit of every key tile.
+// Blocks start with the last query tiles, which see the most keys under the causal mask. P's rounding to bf16
+// is the operand type's; sums and statistics are fp32.
 #include "latent.cuh"
+#include "sm100.cuh"
 
 namespace kda {
 namespace {
 
-// One warp per (query, head): the running maximum and sum over the keys, fp32 throughout.
-__global__ void __launch_bounds__(128) latent_fwd_simple(LatentArgs a)
+using namespace sm100;
+
+constexpr int QT = 128, KT = 128;             // query rows of a tile (two per block), keys of a tile
+constexpr int NT = 8 * 32 + 64, W_LOAD = 8, W_MMA = 9;
+constexpr uint32_t UNIT = 16384;              // 128 rows x 64 channels, 128-byte swizzle
+constexpr int NRING = 8;
+constexpr uint32_t OFF_Q = 0, OFF_RING = 6 * UNIT, OFF_BAR = OFF_RING + NRING * UNIT;
+constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
+static_assert(SMEM <= 232448, "shared memory");
+enum { B_Q, B_FULL, B_EMPTY = B_FULL + NRING, B_S = B_EMPTY + NRING, B_PA = B_S + 2, B_PB = B_PA + 2, B_PV = B_PB + 2,
+       B_DRAIN = B_PV + 2, N_BARS };
+constexpr uint32_t TM_S = 0, TM_O = 256;      // S (and P over it) of the two tiles, O of the two tiles
+
+struct Tile { int n; long long q0, qn, k0, kn; };   // sequence; the block's first query row, rows left, its keys
+
+// Query slot `slot` (256 rows each; slot of sequence n's tile c: floor(first row / 256) + n + c).
+__device__ __forceinline__ bool slot_tile(const LatentArgs &a, long long slot, Tile *t, LatentSpan *s)
 {
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
+    int lo = 0, hi = a.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const long long st = a.cu_q ? (long long)a.cu_q[mid] : (long long)mid * a.T;
+        if (st / (2 * QT) + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    if (!latent_span(a.cu_q, a.cu_k, lo, a.T, a.Tk, s)) return false;
+    const long long c = slot - (s->q0 / (2 * QT) + lo);
+    if (c < 0 || c * 2 * QT >= s->q1 - s->q0) return false;
+    t->n = lo;
+    t->q0 = s->q0 + c * 2 * QT;
+    t->qn = s->q1 - t->q0;
+    t->k0 = s->k0;
+    t->kn = s->k1 - s->k0;
+    return true;
+}
+
+__global__ void __launch_bounds__(NT, 1)
+latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r)
+{
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.H;
+    const long long slot = slots - 1 - blockIdx.x / a.H;
+    if (blockIdx.x == 0) {
         check_offsets(a.cu_q, a.N, a.T, a.status);
         check_offsets(a.cu_k, a.N, a.Tk, a.status);
     }
-    const long long tok = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int h = blockIdx.y, lane = threadIdx.x & 31;
-    if (tok >= (long long)a.B * a.T) return;
-    const int n = latent_sequence(a.cu_q, a.N, a.T, tok);
-    LatentSpan s;
-    if (n < 0 || !latent_span(a.cu_q, a.cu_k, n, a.T, a.Tk, &s)) return;
-    const int W = kHeadDim + a.R;
-    const __nv_bfloat16 *q = a.q + ((size_t)tok * a.H + h) * W;
-    float qv[6] = {}, acc[4] = {};
-    for (int c = 0; c < W / 32; ++c) qv[c] = to_f32(q[c * 32 + lane]);
-    float m = -INFINITY, l = 0.f;
-    const long long hi = a.causal ? min(s.k1 - s.k0, tok - s.q0 + (s.k1 - s.k0) - (s.q1 - s.q0) + 1) : s.k1 - s.k0;
-    for (long long j = 0; j < hi; ++j) {
-        const __nv_bfloat16 *k = a.k + (s.k0 + j) * a.k_tok + h * a.k_head, *v = a.v + (s.k0 + j) * a.v_tok + h * a.v_head;
-        float d = 0.f;
-        for (int c = 0; c < 4; ++c) d += qv[c] * to_f32(k[c * 32 + lane]);
-        if (a.R) for (int c = 0; c < 2; ++c) d += qv[4 + c] * to_f32(a.r[(s.k0 + j) * a.r_tok + c * 32 + lane]);
-        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        d *= a.scale;
-        const float m2 = fmaxf(m, d);
-        if (m2 == -INFINITY) continue;
-        const float f = expf(m - m2), p = expf(d - m2);
-        l = l * f + p;
-        for (int c = 0; c < 4; ++c) acc[c] = acc[c] * f + p * to_f32(v[c * 32 + lane]);
-        m = m2;
+    Tile t;
+    LatentSpan span;
+    if (!slot_tile(a, slot, &t, &span)) return;                        // uniform
+    // tiles of keys that some row of query tile i sees: rows r0 .. of the sequence, row r up to key r + Lk - Lq
+    const long long shift = t.kn - (span.q1 - span.q0), r0 = t.q0 - span.q0;
+    int nt[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const long long last = min(r0 + (i + 1) * QT, span.q1 - span.q0) - 1;      // the tile's last row
+        long long keys = a.causal ? min(t.kn, last + shift + 1) : t.kn;
+        if (i * QT >= t.qn || keys < 0) keys = 0;
+        nt[i] = (int)((keys + KT - 1) / KT);
     }
-    for (int c = 0; c < 4; ++c)
-        a.out[((size_t)tok * a.H + h) * kHeadDim + c * 32 + lane] = __float2bfloat16_rn(l > 0.f ? acc[c] / l : 0.f);
-    if (lane == 0) a.lse[tok * a.H + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    const int ntile = max(nt[0], nt[1]);
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
+    volatile int *ctl = reinterpret_cast<volatile int *>(bars + N_BARS);      // [0] tensor memory, [1] abort
+    if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
+    if (tid == 0) {
+        mbar_init(&bars[B_Q], 1);
+        for (int i = 0; i < NRING; ++i) { mbar_init(&bars[B_FULL + i], 1); mbar_init(&bars[B_EMPTY + i], 1); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[B_S + i], 1);
+            mbar_init(&bars[B_PA + i], 4);
+            mbar_init(&bars[B_PB + i], 4);
+            mbar_init(&bars[B_PV + i], 1);
+        }
+        mbar_init(&bars[B_DRAIN], 1);
+        ctl[1] = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
+    volatile int *abort_flag = ctl + 1;
+    auto wait = [&](int b, uint32_t parity) {
+        if (mbar_try_wait(&bars[b], parity)) return true;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&bars[b], parity)) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > 2000000000LL) { *abort_flag = 1; set_status(a.status, KDA_ERR_TIMEOUT); return false; }
+        }
+        return true;
+    };
+    const int kunits = 2 + (a.R ? 1 : 0);      // units of a key tile; a value tile has two
+
+    if (warp == W_LOAD) {
+        // ============================================================================ loader
+        if (elect_one() && ntile > 0) {
+            tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v);
+            mbar_arrive_expect_tx(&bars[B_Q], 2 * kunits * UNIT);
+            for (int i = 0; i < 2; ++i)
+                for (int u = 0; u < kunits; ++u)
+                    tma_load_3d(sm + OFF_Q + (i * 3 + u) * UNIT, &tm_q, &bars[B_Q], u * 64, (int)(t.q0 + i * QT), h);
+            int s = 0, used = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            auto unit = [&](const CUtensorMap *m, int c, int row, bool shared) {
+                if (used >= NRING) ok = wait(B_EMPTY + s, ph ^ 1);
+                if (!ok) return;
+                mbar_arrive_expect_tx(&bars[B_FULL + s], UNIT);
+                if (shared) tma_load_2d(sm + OFF_RING + s * UNIT, m, &bars[B_FULL + s], c, row);
+                else tma_load_3d(sm + OFF_RING + s * UNIT, m, &bars[B_FULL + s], c, row, h);
+                ++used;
+                if (++s == NRING) { s = 0; ph ^= 1; }
+            };
+            for (int j = 0; j < ntile && ok; ++j) {
+                const int row = (int)(t.k0 + (long long)j * KT);
+                for (int u = 0; u < 2 && ok; ++u) unit(&tm_k, u * 64, row, false);
+                if (a.R && ok) unit(&tm_r, 0, row, true);
+                for (int u = 0; u < 2 && ok; ++u) unit(&tm_v, u * 64, row, false);
+            }
+            if (!ok) {                          // a wait ran out: what is in flight lands before the block ends
+                mbar_wait(&bars[B_Q], 0, 100000000LL);
+                for (int i = max(0, used - NRING); i < used; ++i) mbar_wait(&bars[B_FULL + i % NRING], (i / NRING) & 1, 100000000LL);
+            }
+        }
+    } else if (warp == W_MMA) {
+        // ======================================================================== MMA issuer
+        // The whole warp runs the loop and one thread issues: slots and addresses stay warp-uniform.
+        const bool el = elect_one();
+        constexpr uint32_t id_s = idesc_bf16(QT, KT, 0, 0), id_o = idesc_bf16(QT, 64, 0, 1);
+        constexpr uint32_t hi = desc_hi(1024, SW_128B);
+        const uint32_t q_lo = desc_lo(sbase + OFF_Q, 16), k_lo = desc_lo(sbase + OFF_RING, 16);
+        const int nt0 = __reduce_max_sync(0xffffffffu, nt[0]), nt1 = __reduce_max_sync(0xffffffffu, nt[1]);
+        const int ntu = max(nt0, nt1);
+        int s = 0, ks = 0, vs = 0;              // ring slot of the next unit; of this tile's keys and values
+        uint32_t ph = 0;
+        auto advance = [&](int x) { return x + 1 == NRING ? 0 : x + 1; };
+        auto take = [&](int count) {            // waits for the next `count` units
+            for (int u = 0; u < count; ++u) {
+                wait(B_FULL + s, ph);
+                if (++s == NRING) { s = 0; ph ^= 1; }
+            }
+            tc_fence_after();
+        };
+        auto scores = [&](int i) {
+            int x = ks;
+            for (int u = 0; u < kunits; ++u) {
+                if (el) {
+                    const uint32_t q = q_lo + (i * 3 + u) * (UNIT / 16), k = k_lo + x * (UNIT / 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        umma_ss(tmem + TM_S + i * 128, desc64(q + e * 2, hi), desc64(k + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                }
+                x = advance(x);
+            }
+            if (el) umma_commit(&bars[B_S + i]);
+        };
+        auto release = [&](int x, int count) {
+            for (int u = 0; u < count; ++u) {
+                if (el) umma_commit(&bars[B_EMPTY + x]);
+                x = advance(x);
+            }
+        };
+        if (ntu > 0) {
+            wait(B_Q, 0);
+            ks = s;
+            take(kunits);
+            if (nt0 > 0) scores(0);
+            if (nt1 > 0) scores(1);
+            release(ks, kunits);
+        }
+        for (int j = 0; j < ntu; ++j) {
+            vs = s;
+            take(2);
+            const bool more = j + 1 < ntu;
+            if (more) ks = s;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int nti = i ? nt1 : nt0;
+                if (j < nti) {
+                    // O_i += P_i V, the first 64 keys and then the others, 64 channels at a time
+                    const uint32_t d = tmem + TM_O + i * 128, p = tmem + TM_S + i * 128;
+                    const uint32_t v0 = k_lo + vs * (UNIT / 16), v1 = k_lo + advance(vs) * (UNIT / 16);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        wait(half ? B_PB + i : B_PA + i, j & 1);
+                        tc_fence_after();
+                        if (el) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t acc = (half > 0 || e > 0 || j > 0) ? 1 : 0, step = (half * 4 + e) * 128;
+                                umma_ts(d, p + (half * 4 + e) * 8, desc64(v0 + step, hi), id_o, acc);
+                                umma_ts(d + 64, p + (half * 4 + e) * 8, desc64(v1 + step, hi), id_o, acc);
+                            }
+                        }
+                    }
+                    if (el) umma_commit(&bars[B_PV + i]);
+                }
+                if (i == 0 && more) take(kunits);
+                if (i == 1) release(vs, 2);
+                if (j + 1 < nti) scores(i);
+            }
+            if (more) release(ks, kunits);
+            if (*abort_flag) break;
+        }
+        if (el) {
+            umma_commit(&bars[B_DRAIN]);
+            if (!mbar_wait(&bars[B_DRAIN], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
+        }
+    } else {
+        // ============================================================================ softmax
+        const int i = warp >> 2, quad = warp & 3;
+        const uint32_t lanes = (uint32_t)quad << 21;
+        const uint32_t ts = tmem + TM_S + i * 128 + lanes, to = tmem + TM_O + i * 128 + lanes;
+        const int row = i * QT + quad * 32 + lane;                  // of the block's 256
+        const bool real = row < t.qn;
+        const long long vis = a.causal ? min(t.kn, r0 + row + shift + 1) : t.kn;
+        const int lim = real ? (int)max(0LL, vis) : 0;              // keys this row sees
+        const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
+        const int nti = nt[i];
+        const float sc = a.scale * 1.44269504088896341f;
+        float m = -1e30f, l = 0.f;
+        for (int j = 0; j < nti; ++j) {
+            wait(B_S + i, j & 1);
+            __syncwarp();
+            tc_fence_after();
+            float s[128];
+            tmem_ld64_sync(ts, *reinterpret_cast<float (*)[64]>(s));
+            tmem_ld64_sync(ts + 64, *reinterpret_cast<float (*)[64]>(s + 64));
+            const int kb = j * KT;
+            if (kb + KT > lim_warp) {
+#pragma unroll
+                for (int e = 0; e < 128; ++e) s[e] = kb + e < lim ? s[e] : -INFINITY;
+            }
+            float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int e = 4; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
+            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+            if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                const float up = fmaxf(m, mx), f = up == m ? 1.f : ex2(m - up);
+                m = up;
+                l *= f;
+                if (j > 0) {
+                    wait(B_PV + i, (j - 1) & 1);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 16) {
+                        float o[16];
+                        tmem_ld16_sync(to + c, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] *= f;
+                        tmem_st16(to + c, o);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            // values behind the sequence's last key may be anything: zeros, before the second product reads them
+            if (kb + KT > t.kn) {
+                const int valid = (int)(t.kn - kb), per = kunits + 2;
+                for (int u = 0; u < 2; ++u) {
+                    const int x = j * per + kunits + u;
+                    wait(B_FULL + x % NRING, (x / NRING) & 1);
+                    unsigned char *un = sm + OFF_RING + (x % NRING) * UNIT;
+                    for (int e = quad * 32 + lane; e < (KT - valid) * 8; e += 128)
+                        *reinterpret_cast<uint4 *>(un + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int x = half * 64 + c * 32 + 2 * e;
+                        const float p0 = ex2(s[x] * sc - m), p1 = ex2(s[x + 1] * sc - m);
+                        sum[(2 * e) & 3] += p0;
+                        sum[(2 * e + 1) & 3] += p1;
+                        w[e] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st16u(ts + half * 32 + c * 16, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[(half ? B_PB : B_PA) + i]);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+        const size_t orow = (size_t)(t.q0 + row) * a.H + h;
+        if (nti > 0) {
+            wait(B_PV + i, (nti - 1) & 1);
+            __syncwarp();
+            tc_fence_after();
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {
+            float o[16];
+            if (nti > 0) tmem_ld16_sync(to + c, o);
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = nti > 0 ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+            if (real) {
+                uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + c);
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
+        if (real) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
 bool al(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
@@ -81,8 +381,19 @@ kda_status_t check_latent(const void *q, const void *k, const void *v, const voi
 
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream)
 {
-    const long long tokens = (long long)a.B * a.T;
-    latent_fwd_simple<<<dim3((unsigned)((tokens + 3) / 4), a.H), 128, 0, stream>>>(a);
+    const long long tokens = (long long)a.B * a.T, keys = (long long)a.B * a.Tk, slots = tokens / (2 * QT) + a.N;
+    if (slots * a.H > 0x7fffffffLL) return cudaErrorInvalidValue;
+    const int W = kHeadDim + a.R;
+    CUtensorMap tq = {}, tk = {}, tv = {}, tr = {};
+    if (!bf16_heads_map(&tq, a.q, W, a.H, tokens, W, (long long)a.H * W, 64, QT)) return cudaErrorNotSupported;
+    // without a key no copy is made
+    if (keys > 0 && (!bf16_heads_map(&tk, a.k, kHeadDim, a.H, keys, a.k_head, a.k_tok, 64, KT) ||
+                     !bf16_heads_map(&tv, a.v, kHeadDim, a.H, keys, a.v_head, a.v_tok, 64, KT) ||
+                     (a.R && !bf16_rows_map(&tr, a.r, kSharedDim, keys, a.r_tok, 64, KT))))
+        return cudaErrorNotSupported;
+    const cudaError_t e = cudaFuncSetAttribute(latent_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
+    if (e != cudaSuccess) return e;
+    latent_fwd_kernel<<<(unsigned)(slots * a.H), NT, SMEM, stream>>>(a, slots, tq, tk, tv, tr);
     return cudaGetLastError();
 }
 
