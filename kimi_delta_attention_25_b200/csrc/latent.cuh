@@ -45,6 +45,27 @@ __device__ __forceinline__ int latent_sequence(const int32_t *cu, int N, int T, 
     return (cu[lo] <= tok && tok < cu[lo + 1]) ? lo : -1;
 }
 
+// Tile c of sequence n over offsets `cu` (rows of `tile`) has slot floor(first row / tile) + n + c: unique, and
+// below total / tile + N. The inverse: the sequence and the tile's first row within it; false for a slot that no
+// tile uses, and for offsets that lie outside the tensors.
+__device__ __forceinline__ bool latent_slot(const int32_t *cu, const LatentArgs &a, int L, bool keys, int tile, long long slot,
+                                            int *n, LatentSpan *s, long long *row)
+{
+    int lo = 0, hi = a.N - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        const long long st = cu ? (long long)cu[mid] : (long long)mid * L;
+        if (st / tile + mid <= slot) lo = mid; else hi = mid - 1;
+    }
+    if (!latent_span(a.cu_q, a.cu_k, lo, a.T, a.Tk, s)) return false;
+    const long long first = keys ? s->k0 : s->q0, count = keys ? s->k1 - s->k0 : s->q1 - s->q0;
+    const long long c = slot - (first / tile + lo);
+    if (c < 0 || c * tile >= count) return false;
+    *n = lo;
+    *row = c * tile;
+    return true;
+}
+
 // Records offsets that break the contract (cu[0] = 0, non-decreasing, cu[N] = T). One block's threads.
 __device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T, int32_t *status)
 {
@@ -67,7 +88,7 @@ cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
 struct LatentBwdArgs {
     const __nv_bfloat16 *dout;
     __nv_bfloat16 *dq, *dk, *dv, *dr;     // dense
-    float *delta;                         // [tokens, H]: dout . out
+    float *stat;                          // [2][H][tokens]: lse in the log2 domain (+infinity for empty rows), dout . out
     float *dr_head;                       // [keys, H, R]: each head's part of the shared key's gradient
 };
 cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaStream_t stream);

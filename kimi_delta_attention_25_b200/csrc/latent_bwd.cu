@@ -1,18 +1,40 @@
 // latent_bwd.cu -- the backward pass of the expanded latent attention (latent_fwd.cu), with P recomputed
 // from the forward's lse:  P = exp(s - lse),  D_i = do_i . o_i,  dP = do v^T,  dS = P (dP - D),
 //   dq = scale dS [k, r],  dk = scale dS^T q[:128],  dr = scale sum_h dS^T q[128:],  dv = P^T do.
+//
+// Three kernels, each for one row of tiles, none of them adding to memory that another block adds to:
+//   dq: rows of 128 queries, over key tiles:    S = Q [K, R]^T, dP = dO V^T,     dq += dS [K, R]
+//   dk: rows of 128 keys, over query tiles:     S^T = [K, R] Q^T, dP^T = V dO^T, dk += dS^T Q
+//   dv: rows of 2 x 128 keys, over query tiles: S^T, dv += P^T dO
+// (the first two are one template: resident operands A1, A2 and streamed ones B1, B2 swap roles). One kernel
+// for dk and dv would need S^T, dP^T, dk (192 columns) and dv in tensor memory: 576 of 512 columns; with query
+// tiles of 64, which fit, the products over 64 columns read their 128-row operand from shared memory twice as
+// often and cost as much as computing S^T again. A fused dq would need atomic sums or 2 bytes of dS per pair in
+// memory, read and written: about twice the time of recomputing S and dP.
+// The tensor cores bound it: per 128 x 128 tile and head 804 + 536 + 792 cycles for dq and dk each and
+// 804 + 536 for dv, 5600 in all, where a single pass without the recomputation would take 3460.
+// dS (and P) pass through tensor memory in bf16 as A operands; sums, lse and D are fp32.
 #include "latent.cuh"
+#include "sm100.cuh"
 
 namespace kda {
 namespace {
 
-// D_i = do_i . o_i, one warp per (token, head).
-__global__ void __launch_bounds__(256) latent_delta_kernel(const __nv_bfloat16 *__restrict__ out, const __nv_bfloat16 *__restrict__ dout,
-                                                           float *__restrict__ delta, long long rows)
+using namespace sm100;
+
+constexpr int TL = 128;                       // rows and columns of a tile
+constexpr int NT = 8 * 32 + 64, W_LOAD = 8, W_MMA = 9;
+constexpr uint32_t UNIT = 16384;              // 128 rows x 64 channels, 128-byte swizzle
+constexpr uint32_t SMEM_MAX = 232448;
+
+// lse in the log2 domain and D_i = do_i . o_i as [H][tokens] (the dk and dv kernels read them along the
+// tokens), one warp per (token, head).
+__global__ void __launch_bounds__(256) latent_stat_kernel(const __nv_bfloat16 *__restrict__ out, const __nv_bfloat16 *__restrict__ dout,
+                                                          const float *__restrict__ lse, float *__restrict__ stat, long long tokens, int H)
 {
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
+    if (row >= tokens * H) return;
     const uint2 o = reinterpret_cast<const uint2 *>(out + row * kHeadDim)[lane], d = reinterpret_cast<const uint2 *>(dout + row * kHeadDim)[lane];
     float s = __uint_as_float(o.x << 16) * __uint_as_float(d.x << 16);
     s += __uint_as_float(o.x & 0xFFFF0000u) * __uint_as_float(d.x & 0xFFFF0000u);
@@ -20,85 +42,601 @@ __global__ void __launch_bounds__(256) latent_delta_kernel(const __nv_bfloat16 *
     s += __uint_as_float(o.y & 0xFFFF0000u) * __uint_as_float(d.y & 0xFFFF0000u);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    if (lane == 0) delta[row] = s;
+    if (lane == 0) {
+        const long long at = (row % H) * tokens + row / H;
+        const float l = lse[row];
+        stat[at] = l == -INFINITY ? INFINITY : l * 1.44269504088896341f;
+        stat[tokens * H + at] = s;
+    }
 }
 
-__device__ __forceinline__ float warp_sum(float x)
-{
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-    return x;
-}
+// ------------------------------------------------------------------------------------ dq and dk
+// Shared memory: A1 (3 units), A2 (2), a ring of 7 units for B1 and one of 2 for B2, the statistics of the
+// columns (dk: two tiles of 128 values of each kind).
+constexpr int N1 = 7, N2 = 2;
+constexpr uint32_t G_A1 = 0, G_A2 = 3 * UNIT, G_B1 = 5 * UNIT, G_B2 = G_B1 + N1 * UNIT, G_STAT = G_B2 + N2 * UNIT,
+                   G_BAR = G_STAT + 2048, G_END = G_BAR + 320;
+static_assert(G_END <= SMEM_MAX, "shared memory");
+enum { G_RES, G_F1, G_E1 = G_F1 + N1, G_F2 = G_E1 + N1, G_E2 = G_F2 + N2, G_S = G_E2 + N2, G_SFREE, G_P, G_PFREE, G_DS,
+       G_ACC, G_DRAIN, G_NBARS };
+static_assert(G_NBARS * 8 + 16 <= 320, "barriers");
+constexpr uint32_t TM_S = 0, TM_P = 128, TM_DS = 256, TM_ACC = 320;
 
-// One warp per (query, head): dq.
-__global__ void __launch_bounds__(128) latent_dq_simple(LatentArgs a, LatentBwdArgs b)
+struct GradMaps { CUtensorMap a1, a1r, a2, b1, b1r, b2; };   // dq: q, -, dout, k, r, v; dk: k, r, v, q, -, dout
+
+// S(j + 1), then the accumulating product of tile j, then dP(j + 1): each product's operands are ready by the
+// time its turn comes (dS(j) is formed from dP(j) while S(j + 1) runs), and the units of B1 that the
+// accumulation frees one by one are filled again before S(j + 2) needs them.
+template <bool DQ>
+__global__ void __launch_bounds__(NT, 1)
+latent_grad_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_constant__ GradMaps maps)
 {
-    if (blockIdx.x == 0 && blockIdx.y == 0) {
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const uint32_t sbase = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.H;
+    const long long slot = DQ ? slots - 1 - blockIdx.x / a.H : blockIdx.x / a.H;   // the longest rows of tiles first
+    if (blockIdx.x == 0) {
         check_offsets(a.cu_q, a.N, a.T, a.status);
         check_offsets(a.cu_k, a.N, a.Tk, a.status);
     }
-    const long long tok = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int h = blockIdx.y, lane = threadIdx.x & 31;
-    if (tok >= (long long)a.B * a.T) return;
-    const int n = latent_sequence(a.cu_q, a.N, a.T, tok);
-    LatentSpan s;
-    if (n < 0 || !latent_span(a.cu_q, a.cu_k, n, a.T, a.Tk, &s)) return;
-    const int W = kHeadDim + a.R;
-    float qv[6] = {}, dov[4], acc[6] = {};
-    for (int c = 0; c < W / 32; ++c) qv[c] = to_f32(a.q[((size_t)tok * a.H + h) * W + c * 32 + lane]);
-    for (int c = 0; c < 4; ++c) dov[c] = to_f32(b.dout[((size_t)tok * a.H + h) * kHeadDim + c * 32 + lane]);
-    const float lse = a.lse[tok * a.H + h], delta = b.delta[tok * a.H + h];
-    const long long hi = a.causal ? min(s.k1 - s.k0, tok - s.q0 + (s.k1 - s.k0) - (s.q1 - s.q0) + 1) : s.k1 - s.k0;
-    for (long long j = 0; j < hi; ++j) {
-        const __nv_bfloat16 *k = a.k + (s.k0 + j) * a.k_tok + h * a.k_head, *v = a.v + (s.k0 + j) * a.v_tok + h * a.v_head;
-        const __nv_bfloat16 *r = a.r + (s.k0 + j) * a.r_tok;
-        float d = 0.f, dp = 0.f;
-        for (int c = 0; c < 4; ++c) { d += qv[c] * to_f32(k[c * 32 + lane]); dp += dov[c] * to_f32(v[c * 32 + lane]); }
-        if (a.R) for (int c = 0; c < 2; ++c) d += qv[4 + c] * to_f32(r[c * 32 + lane]);
-        d = warp_sum(d) * a.scale;
-        dp = warp_sum(dp);
-        const float ds = (lse == -INFINITY ? 0.f : expf(d - lse)) * (dp - delta) * a.scale;
-        for (int c = 0; c < 4; ++c) acc[c] += ds * to_f32(k[c * 32 + lane]);
-        if (a.R) for (int c = 0; c < 2; ++c) acc[4 + c] += ds * to_f32(r[c * 32 + lane]);
+    if (sbase & 1023u) { if (tid == 0) set_status(a.status, KDA_ERR_CUDA); return; }   // the swizzle needs it (it holds)
+    int n;
+    LatentSpan sp;
+    long long r0;
+    if (!latent_slot(DQ ? a.cu_q : a.cu_k, a, DQ ? a.T : a.Tk, !DQ, TL, slot, &n, &sp, &r0)) return;   // uniform
+    const long long Lq = sp.q1 - sp.q0, Lk = sp.k1 - sp.k0, shift = Lk - Lq;
+    const long long row_first = (DQ ? sp.q0 : sp.k0) + r0, rows = (DQ ? Lq : Lk) - r0;     // rows: may exceed the tile
+    const long long col_first = DQ ? sp.k0 : sp.q0, cols = DQ ? Lk : Lq;
+    // tiles of the other side that some row of this one meets
+    int t_lo = 0, t_hi;
+    if (DQ) {
+        long long keys = a.causal ? min(Lk, min(r0 + TL, Lq) + shift) : Lk;
+        t_hi = keys > 0 ? (int)((keys + TL - 1) / TL) : 0;
+    } else {
+        const long long q = a.causal ? max(0LL, r0 - shift) : 0;           // first query that sees the first key here
+        t_lo = (int)(min(q, Lq) / TL);
+        t_hi = q < Lq ? (int)((Lq + TL - 1) / TL) : t_lo;
     }
-    for (int c = 0; c < W / 32; ++c) b.dq[((size_t)tok * a.H + h) * W + c * 32 + lane] = __float2bfloat16_rn(acc[c]);
+    const int nt = t_hi - t_lo;
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G_BAR);
+    volatile int *ctl = reinterpret_cast<volatile int *>(bars + G_NBARS);      // [0] tensor memory, [1] abort
+    if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
+    if (tid == 0) {
+        for (int i = 0; i < G_NBARS; ++i) mbar_init(&bars[i], (i == G_SFREE || i == G_PFREE || i == G_DS) ? 8 : 1);
+        ctl[1] = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
+    volatile int *abort_flag = ctl + 1;
+    auto wait = [&](int x, uint32_t parity) {
+        if (mbar_try_wait(&bars[x], parity)) return true;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&bars[x], parity)) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > 2000000000LL) { *abort_flag = 1; set_status(a.status, KDA_ERR_TIMEOUT); return false; }
+        }
+        return true;
+    };
+    const int u1 = 2 + (a.R ? 1 : 0);          // units of A1 and of a tile of B1; A2 and B2 have two
+
+    if (warp == W_LOAD) {
+        // ============================================================================ loader
+        if (elect_one() && nt > 0) {
+            // units of keys with their shared part, or of whole query rows
+            auto load1 = [&](bool key_side, const CUtensorMap *m, const CUtensorMap *mr, unsigned char *dst, uint64_t *bar, int u, int row) {
+                if (key_side && u == 2) tma_load_2d(dst, mr, bar, 0, row);
+                else tma_load_3d(dst, m, bar, u * 64, row, h);
+            };
+            mbar_arrive_expect_tx(&bars[G_RES], (u1 + 2) * UNIT);
+            for (int u = 0; u < u1; ++u) load1(!DQ, &maps.a1, &maps.a1r, sm + G_A1 + u * UNIT, &bars[G_RES], u, (int)row_first);
+            for (int u = 0; u < 2; ++u) tma_load_3d(sm + G_A2 + u * UNIT, &maps.a2, &bars[G_RES], u * 64, (int)row_first, h);
+            int s1 = 0, s2 = 0, used1 = 0, used2 = 0;
+            uint32_t p1 = 0, p2 = 0;
+            bool ok = true;
+            for (int j = 0; j < nt && ok; ++j) {
+                const int row = (int)(col_first + (long long)(t_lo + j) * TL);
+                for (int u = 0; u < u1 && ok; ++u) {
+                    if (used1 >= N1) ok = wait(G_E1 + s1, p1 ^ 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars[G_F1 + s1], UNIT);
+                    load1(DQ, &maps.b1, &maps.b1r, sm + G_B1 + s1 * UNIT, &bars[G_F1 + s1], u, row);
+                    ++used1;
+                    if (++s1 == N1) { s1 = 0; p1 ^= 1; }
+                }
+                for (int u = 0; u < 2 && ok; ++u) {
+                    if (used2 >= N2) ok = wait(G_E2 + s2, p2 ^ 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars[G_F2 + s2], UNIT);
+                    tma_load_3d(sm + G_B2 + s2 * UNIT, &maps.b2, &bars[G_F2 + s2], u * 64, row, h);
+                    ++used2;
+                    if (++s2 == N2) { s2 = 0; p2 ^= 1; }
+                }
+            }
+            if (!ok) {                          // a wait ran out: what is in flight lands before the block ends
+                mbar_wait(&bars[G_RES], 0, 100000000LL);
+                for (int i = max(0, used1 - N1); i < used1; ++i) mbar_wait(&bars[G_F1 + i % N1], (i / N1) & 1, 100000000LL);
+                for (int i = max(0, used2 - N2); i < used2; ++i) mbar_wait(&bars[G_F2 + i % N2], (i / N2) & 1, 100000000LL);
+            }
+        }
+    } else if (warp == W_MMA) {
+        // ======================================================================== MMA issuer
+        const bool el = elect_one();
+        constexpr uint32_t id_s = idesc_bf16(TL, TL, 0, 0), id_a = idesc_bf16(TL, 64, 0, 1);
+        constexpr uint32_t hi = desc_hi(1024, SW_128B);
+        const uint32_t a1_lo = desc_lo(sbase + G_A1, 16), a2_lo = desc_lo(sbase + G_A2, 16);
+        const uint32_t b1_lo = desc_lo(sbase + G_B1, 16), b2_lo = desc_lo(sbase + G_B2, 16);
+        const int ntu = __reduce_max_sync(0xffffffffu, nt);
+        int s1 = 0, c1 = 0, s2 = 0;             // ring slots: B1 for the scores, B1 for the accumulation, B2
+        uint32_t p1 = 0, p2 = 0;
+        auto scores = [&]() {
+            for (int u = 0; u < u1; ++u) {
+                wait(G_F1 + s1, p1);
+                tc_fence_after();
+                if (el) {
+                    const uint32_t x = a1_lo + u * (UNIT / 16), y = b1_lo + s1 * (UNIT / 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        umma_ss(tmem + TM_S, desc64(x + e * 2, hi), desc64(y + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                }
+                if (++s1 == N1) { s1 = 0; p1 ^= 1; }
+            }
+            if (el) umma_commit(&bars[G_S]);
+        };
+        auto dp = [&]() {
+            for (int u = 0; u < 2; ++u) {
+                wait(G_F2 + s2, p2);
+                tc_fence_after();
+                if (el) {
+                    const uint32_t x = a2_lo + u * (UNIT / 16), y = b2_lo + s2 * (UNIT / 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        umma_ss(tmem + TM_P, desc64(x + e * 2, hi), desc64(y + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                    umma_commit(&bars[G_E2 + s2]);
+                }
+                if (++s2 == N2) { s2 = 0; p2 ^= 1; }
+            }
+            if (el) umma_commit(&bars[G_P]);
+        };
+        if (ntu > 0) {
+            wait(G_RES, 0);
+            scores();
+            dp();
+        }
+        for (int j = 0; j < ntu; ++j) {
+            if (j + 1 < ntu) {
+                wait(G_SFREE, j & 1);
+                scores();
+            }
+            wait(G_DS, j & 1);
+            tc_fence_after();
+            for (int u = 0; u < u1; ++u) {
+                if (el) {
+                    const uint32_t y = b1_lo + c1 * (UNIT / 16);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        umma_ts(tmem + TM_ACC + u * 64, tmem + TM_DS + e * 8, desc64(y + e * 128, hi), id_a, (e > 0 || j > 0) ? 1 : 0);
+                    umma_commit(&bars[G_E1 + c1]);
+                }
+                if (++c1 == N1) c1 = 0;
+            }
+            if (el) umma_commit(&bars[G_ACC]);
+            if (j + 1 < ntu) {
+                wait(G_PFREE, j & 1);
+                dp();
+            }
+            if (*abort_flag) break;
+        }
+        if (el) {
+            umma_commit(&bars[G_DRAIN]);
+            if (!mbar_wait(&bars[G_DRAIN], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
+        }
+    } else {
+        // ============================================================================ P and dS
+        // Lane = row; the two warpgroups share the columns.
+        const int g = warp >> 2, quad = warp & 3;
+        const uint32_t lanes = (uint32_t)quad << 21;
+        const int row = quad * 32 + lane;
+        const bool real = row < rows;
+        const float sc = a.scale * 1.44269504088896341f;
+        const long long tokens = (long long)a.B * a.T;
+        const float *st_lse = b.stat + (size_t)h * tokens, *st_d = st_lse + (size_t)tokens * a.H;
+        float lse_r = 0.f, d_r = 0.f;                        // dq: this row's
+        if (DQ && real) { lse_r = st_lse[row_first + row]; d_r = st_d[row_first + row]; }
+        // columns this row meets: [lo, hi) of the sequence
+        long long lo = 0, hi = real ? cols : 0;
+        if (a.causal) {
+            if (DQ) hi = min(hi, r0 + row + shift + 1);
+            else lo = r0 + row - shift;
+        }
+        const int lo_w = __reduce_max_sync(0xffffffffu, (int)max(lo, 0LL)), hi_w = __reduce_min_sync(0xffffffffu, (int)max(hi, 0LL));
+        float *stat = reinterpret_cast<float *>(sm + G_STAT);
+        // dk: each warpgroup keeps its columns' statistics, [buffer][group][lse, D][64]
+        float next = 0.f;
+        auto fetch = [&](int j) {
+            const int t = tid & 127;
+            const long long c = (long long)(t_lo + j) * TL + g * 64 + (t & 63);
+            next = c < cols ? (t < 64 ? st_lse : st_d)[col_first + c] : 0.f;
+        };
+        if (!DQ && nt > 0) fetch(0);
+        for (int j = 0; j < nt; ++j) {
+            float *sj = stat + ((j & 1) * 2 + g) * 128;
+            if (!DQ) {
+                sj[tid & 127] = next;
+                if (j + 1 < nt) fetch(j + 1);
+                named_bar_sync(1 + g, 128);
+            }
+            const long long c0 = (long long)(t_lo + j) * TL + g * 64;
+            const bool edge = c0 < lo_w || c0 + 64 > hi_w;
+            wait(G_S, j & 1);
+            __syncwarp();
+            tc_fence_after();
+            float p[64];
+            tmem_ld64_sync(tmem + TM_S + lanes + g * 64, p);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[G_SFREE]);
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) {
+                float4 l4 = make_float4(lse_r, lse_r, lse_r, lse_r);
+                if (!DQ) l4 = *reinterpret_cast<const float4 *>(sj + e);
+                p[e] = ex2(p[e] * sc - l4.x);
+                p[e + 1] = ex2(p[e + 1] * sc - l4.y);
+                p[e + 2] = ex2(p[e + 2] * sc - l4.z);
+                p[e + 3] = ex2(p[e + 3] * sc - l4.w);
+            }
+            // rows of B1 behind the sequence's end may be anything: zeros, before the accumulation reads them
+            // (its rows are this tile's columns; each warpgroup clears its own)
+            const int valid = (int)min((long long)TL, cols - (long long)(t_lo + j) * TL);
+            if (valid < (g + 1) * 64) {
+                const int from = max(valid, g * 64);
+                for (int u = 0; u < u1; ++u) {
+                    unsigned char *un = sm + G_B1 + (uint32_t)((j * u1 + u) % N1) * UNIT;
+                    for (int e = tid & 127; e < ((g + 1) * 64 - from) * 8; e += 128)
+                        *reinterpret_cast<uint4 *>(un + from * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            wait(G_P, j & 1);
+            __syncwarp();
+            tc_fence_after();
+            uint32_t w[32];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float d[32];
+                tmem_ld32_sync(tmem + TM_P + lanes + g * 64 + half * 32, d);
+                if (half) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars[G_PFREE]);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    float4 d4 = make_float4(d_r, d_r, d_r, d_r);
+                    if (!DQ) d4 = *reinterpret_cast<const float4 *>(sj + 64 + half * 32 + e);
+                    float *x = p + half * 32 + e;
+                    d[e] = x[0] * (d[e] - d4.x);
+                    d[e + 1] = x[1] * (d[e + 1] - d4.y);
+                    d[e + 2] = x[2] * (d[e + 2] - d4.z);
+                    d[e + 3] = x[3] * (d[e + 3] - d4.w);
+                }
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const long long c = c0 + half * 32 + e;
+                        if (c < lo || c >= hi) d[e] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[half * 16 + e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
+            }
+            if (j > 0) { wait(G_ACC, (j - 1) & 1); __syncwarp(); }       // dS was last read by the product of tile j - 1
+            tmem_st32(tmem + TM_DS + lanes + g * 32, w);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[G_DS]);
+        }
+        if (nt > 0) {
+            wait(G_ACC, (nt - 1) & 1);
+            __syncwarp();
+            tc_fence_after();
+        }
+        // results: chunks of 16 columns, the two warpgroups in turn
+        const size_t at = (size_t)(row_first + row) * a.H + h;
+#pragma unroll 1
+        for (int c = g * 16; c < u1 * 64; c += 32) {
+            float o[16];
+            if (nt > 0) tmem_ld16_sync(tmem + TM_ACC + lanes + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = nt > 0 ? o[e] * a.scale : 0.f;
+            if (!real) continue;
+            if (!DQ && c >= kHeadDim) {
+                float4 *dst = reinterpret_cast<float4 *>(b.dr_head + at * kSharedDim + c - kHeadDim);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            } else {
+                uint4 *dst = reinterpret_cast<uint4 *>(DQ ? b.dq + at * (kHeadDim + a.R) + c : b.dk + at * kHeadDim + c);
+                dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+                dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]), pack_bf16x2(o[14], o[15]));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
-// One warp per (key, head): dk, dv and the head's part of dr.
-__global__ void __launch_bounds__(128) latent_dkv_simple(LatentArgs a, LatentBwdArgs b)
+// ------------------------------------------------------------------------------------------ dv
+// The forward kernel's structure with the roles of queries and keys exchanged and lse known: two key tiles at
+// once, P^T over S^T's columns as the A operand of dv += P^T dO.
+constexpr int NV = 8;
+constexpr uint32_t V_A = 0, V_RING = 6 * UNIT, V_STAT = V_RING + NV * UNIT, V_BAR = V_STAT + 1024, V_END = V_BAR + 320;
+static_assert(V_END <= SMEM_MAX, "shared memory");
+enum { V_RES, V_F, V_E = V_F + NV, V_S = V_E + NV, V_PA = V_S + 2, V_PB = V_PA + 2, V_PV = V_PB + 2, V_DRAIN = V_PV + 2, V_NBARS };
+constexpr uint32_t TV_S = 0, TV_O = 256;
+
+__global__ void __launch_bounds__(NT, 1)
+latent_dv_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_constant__ GradMaps maps)
 {
-    const long long key = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int h = blockIdx.y, lane = threadIdx.x & 31;
-    if (key >= (long long)a.B * a.Tk) return;
-    const int n = latent_sequence(a.cu_k, a.N, a.Tk, key);
-    LatentSpan s;
-    if (n < 0 || !latent_span(a.cu_q, a.cu_k, n, a.T, a.Tk, &s)) return;
-    const int W = kHeadDim + a.R;
-    float kv[6] = {}, vv[4], dk[6] = {}, dv[4] = {};
-    for (int c = 0; c < 4; ++c) {
-        kv[c] = to_f32(a.k[key * a.k_tok + h * a.k_head + c * 32 + lane]);
-        vv[c] = to_f32(a.v[key * a.v_tok + h * a.v_head + c * 32 + lane]);
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const uint32_t sbase = smem_u32(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % a.H;
+    if (sbase & 1023u) { if (tid == 0) set_status(a.status, KDA_ERR_CUDA); return; }
+    int n;
+    LatentSpan sp;
+    long long r0;
+    if (!latent_slot(a.cu_k, a, a.Tk, true, 2 * TL, blockIdx.x / a.H, &n, &sp, &r0)) return;   // uniform
+    const long long Lq = sp.q1 - sp.q0, Lk = sp.k1 - sp.k0, shift = Lk - Lq, rows = Lk - r0;
+    const long long row_first = sp.k0 + r0;
+    // query tiles that see some key of tile i: from the first that sees its first key to the last
+    int first[2];
+    const int t_hi = (int)((Lq + TL - 1) / TL);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const long long q = a.causal ? max(0LL, r0 + i * TL - shift) : 0;
+        first[i] = (q < Lq && i * TL < rows) ? (int)(q / TL) : t_hi;
     }
-    if (a.R) for (int c = 0; c < 2; ++c) kv[4 + c] = to_f32(a.r[key * a.r_tok + c * 32 + lane]);
-    long long lo = a.causal ? (key - s.k0) - (s.k1 - s.k0) + (s.q1 - s.q0) : 0;
-    if (lo < 0) lo = 0;
-    for (long long tok = s.q0 + lo; tok < s.q1; ++tok) {
-        const __nv_bfloat16 *q = a.q + ((size_t)tok * a.H + h) * W, *dout = b.dout + ((size_t)tok * a.H + h) * kHeadDim;
-        float qv[6] = {}, dov[4], d = 0.f, dp = 0.f;
-        for (int c = 0; c < W / 32; ++c) { qv[c] = to_f32(q[c * 32 + lane]); d += qv[c] * kv[c]; }
-        for (int c = 0; c < 4; ++c) { dov[c] = to_f32(dout[c * 32 + lane]); dp += dov[c] * vv[c]; }
-        d = warp_sum(d) * a.scale;
-        dp = warp_sum(dp);
-        const float lse = a.lse[tok * a.H + h], p = lse == -INFINITY ? 0.f : expf(d - lse);
-        const float ds = p * (dp - b.delta[tok * a.H + h]) * a.scale;
-        for (int c = 0; c < W / 32; ++c) dk[c] += ds * qv[c];
-        for (int c = 0; c < 4; ++c) dv[c] += p * dov[c];
+    const int t_lo = min(first[0], first[1]);                  // tile 1 starts no earlier than tile 0, or has no rows
+    const int nt = t_hi - t_lo;
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + V_BAR);
+    volatile int *ctl = reinterpret_cast<volatile int *>(bars + V_NBARS);
+    if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
+    if (tid == 0) {
+        for (int i = 0; i < V_NBARS; ++i) mbar_init(&bars[i], (i >= V_PA && i < V_PV) ? 4 : 1);
+        ctl[1] = 0;
+        fence_mbar_init();
     }
-    for (int c = 0; c < 4; ++c) {
-        b.dk[((size_t)key * a.H + h) * kHeadDim + c * 32 + lane] = __float2bfloat16_rn(dk[c]);
-        b.dv[((size_t)key * a.H + h) * kHeadDim + c * 32 + lane] = __float2bfloat16_rn(dv[c]);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
+    volatile int *abort_flag = ctl + 1;
+    auto wait = [&](int x, uint32_t parity) {
+        if (mbar_try_wait(&bars[x], parity)) return true;
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&bars[x], parity)) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > 2000000000LL) { *abort_flag = 1; set_status(a.status, KDA_ERR_TIMEOUT); return false; }
+        }
+        return true;
+    };
+    const int u1 = 2 + (a.R ? 1 : 0);
+
+    if (warp == W_LOAD) {
+        // ============================================================================ loader
+        if (elect_one() && nt > 0) {
+            mbar_arrive_expect_tx(&bars[V_RES], 2 * u1 * UNIT);
+            for (int i = 0; i < 2; ++i)
+                for (int u = 0; u < u1; ++u) {
+                    unsigned char *dst = sm + V_A + (i * 3 + u) * UNIT;
+                    if (u == 2) tma_load_2d(dst, &maps.a1r, &bars[V_RES], 0, (int)(row_first + i * TL));
+                    else tma_load_3d(dst, &maps.a1, &bars[V_RES], u * 64, (int)(row_first + i * TL), h);
+                }
+            int s = 0, used = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            for (int j = 0; j < nt && ok; ++j) {
+                const int row = (int)(sp.q0 + (long long)(t_lo + j) * TL);
+                for (int u = 0; u < u1 + 2 && ok; ++u) {
+                    if (used >= NV) ok = wait(V_E + s, ph ^ 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bars[V_F + s], UNIT);
+                    tma_load_3d(sm + V_RING + s * UNIT, u < u1 ? &maps.b1 : &maps.b2, &bars[V_F + s], (u < u1 ? u : u - u1) * 64, row, h);
+                    ++used;
+                    if (++s == NV) { s = 0; ph ^= 1; }
+                }
+            }
+            if (!ok) {
+                mbar_wait(&bars[V_RES], 0, 100000000LL);
+                for (int i = max(0, used - NV); i < used; ++i) mbar_wait(&bars[V_F + i % NV], (i / NV) & 1, 100000000LL);
+            }
+        }
+    } else if (warp == W_MMA) {
+        // ======================================================================== MMA issuer
+        const bool el = elect_one();
+        constexpr uint32_t id_s = idesc_bf16(TL, TL, 0, 0), id_o = idesc_bf16(TL, 64, 0, 1);
+        constexpr uint32_t hi = desc_hi(1024, SW_128B);
+        const uint32_t a_lo = desc_lo(sbase + V_A, 16), r_lo = desc_lo(sbase + V_RING, 16);
+        const int ntu = __reduce_max_sync(0xffffffffu, nt);
+        const int f0 = __reduce_max_sync(0xffffffffu, first[0] - t_lo), f1 = __reduce_max_sync(0xffffffffu, first[1] - t_lo);
+        int s = 0, qs = 0, os = 0;
+        uint32_t ph = 0;
+        auto advance = [&](int x) { return x + 1 == NV ? 0 : x + 1; };
+        auto take = [&](int count) {
+            for (int u = 0; u < count; ++u) {
+                wait(V_F + s, ph);
+                if (++s == NV) { s = 0; ph ^= 1; }
+            }
+            tc_fence_after();
+        };
+        auto scores = [&](int i) {
+            int x = qs;
+            for (int u = 0; u < u1; ++u) {
+                if (el) {
+                    const uint32_t k = a_lo + (i * 3 + u) * (UNIT / 16), q = r_lo + x * (UNIT / 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        umma_ss(tmem + TV_S + i * 128, desc64(k + e * 2, hi), desc64(q + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                }
+                x = advance(x);
+            }
+            if (el) umma_commit(&bars[V_S + i]);
+        };
+        auto release = [&](int x, int count) {
+            for (int u = 0; u < count; ++u) {
+                if (el) umma_commit(&bars[V_E + x]);
+                x = advance(x);
+            }
+        };
+        if (ntu > 0) {
+            wait(V_RES, 0);
+            qs = s;
+            take(u1);
+            if (f0 == 0) scores(0);
+            if (f1 == 0) scores(1);
+            release(qs, u1);
+        }
+        for (int j = 0; j < ntu; ++j) {
+            os = s;
+            take(2);
+            const bool more = j + 1 < ntu;
+            if (more) qs = s;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int f = i ? f1 : f0;
+                if (j >= f) {
+                    const uint32_t d = tmem + TV_O + i * 128, p = tmem + TV_S + i * 128;
+                    const uint32_t v0 = r_lo + os * (UNIT / 16), v1 = r_lo + advance(os) * (UNIT / 16);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        wait((half ? V_PB : V_PA) + i, (j - f) & 1);
+                        tc_fence_after();
+                        if (el) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t acc = (half > 0 || e > 0 || j > f) ? 1 : 0, step = (half * 4 + e) * 128;
+                                umma_ts(d, p + (half * 4 + e) * 8, desc64(v0 + step, hi), id_o, acc);
+                                umma_ts(d + 64, p + (half * 4 + e) * 8, desc64(v1 + step, hi), id_o, acc);
+                            }
+                        }
+                    }
+                    if (el) umma_commit(&bars[V_PV + i]);
+                }
+                if (i == 0 && more) take(u1);
+                if (i == 1) release(os, 2);
+                if (more && j + 1 >= f) scores(i);
+            }
+            if (more) release(qs, u1);
+            if (*abort_flag) break;
+        }
+        if (el) {
+            umma_commit(&bars[V_DRAIN]);
+            if (!mbar_wait(&bars[V_DRAIN], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
+        }
+    } else {
+        // ============================================================================ P
+        const int i = warp >> 2, quad = warp & 3;
+        const uint32_t lanes = (uint32_t)quad << 21;
+        const uint32_t ts = tmem + TV_S + i * 128 + lanes, to = tmem + TV_O + i * 128 + lanes;
+        const int row = i * TL + quad * 32 + lane;                  // of the block's 256 keys
+        const bool real = row < rows;
+        const float sc = a.scale * 1.44269504088896341f;
+        const float *st_lse = b.stat + (size_t)h * ((long long)a.B * a.T);
+        const long long lo = a.causal ? r0 + row - shift : 0;       // first query that sees this key
+        const int lo_w = __reduce_max_sync(0xffffffffu, (int)max(lo, 0LL));
+        float *stat = reinterpret_cast<float *>(sm + V_STAT) + i * TL;
+        const int f = first[i];
+        float next = 0.f;
+        auto fetch = [&](int tile) {
+            const long long c = (long long)tile * TL + (tid & 127);
+            next = c < Lq ? st_lse[sp.q0 + c] : INFINITY;
+        };
+        if (f < t_hi) fetch(f);
+        for (int tile = f; tile < t_hi; ++tile) {
+            const int j = tile - f;
+            named_bar_sync(1 + i, 128);                             // the last tile's statistics are read
+            stat[tid & 127] = next;
+            if (tile + 1 < t_hi) fetch(tile + 1);
+            named_bar_sync(1 + i, 128);
+            const long long c0 = (long long)tile * TL;
+            const bool edge = c0 < lo_w || c0 + TL > Lq;
+            wait(V_S + i, j & 1);
+            __syncwarp();
+            tc_fence_after();
+            // gradients of rows behind the sequence's last query may be anything: zeros, before the product reads them
+            // (behind the wait for the scores: the ring slots' earlier uses are over by then, so the parity is this use's)
+            if (c0 + TL > Lq) {
+                const int valid = (int)(Lq - c0), per = u1 + 2;
+                for (int u = 0; u < 2; ++u) {
+                    const int x = (tile - t_lo) * per + u1 + u;
+                    wait(V_F + x % NV, (x / NV) & 1);
+                    unsigned char *un = sm + V_RING + (x % NV) * UNIT;
+                    for (int e = quad * 32 + lane; e < (TL - valid) * 8; e += 128)
+                        *reinterpret_cast<uint4 *>(un + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            float s[128];
+            tmem_ld64_sync(ts, *reinterpret_cast<float (*)[64]>(s));
+            tmem_ld64_sync(ts + 64, *reinterpret_cast<float (*)[64]>(s + 64));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (edge) {
+#pragma unroll
+                    for (int e = half * 64; e < half * 64 + 64; ++e) {
+                        const long long c = c0 + e;
+                        if (c < lo || c >= Lq) s[e] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const int x = half * 64 + c * 32 + 2 * e;
+                        const float4 l4 = *reinterpret_cast<const float4 *>(stat + x);
+                        w[e] = pack_bf16x2(ex2(s[x] * sc - l4.x), ex2(s[x + 1] * sc - l4.y));
+                        w[e + 1] = pack_bf16x2(ex2(s[x + 2] * sc - l4.z), ex2(s[x + 3] * sc - l4.w));
+                    }
+                    tmem_st16u(ts + half * 32 + c * 16, w);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[(half ? V_PB : V_PA) + i]);
+            }
+        }
+        const int cnt = t_hi - f;
+        if (cnt > 0) {
+            wait(V_PV + i, (cnt - 1) & 1);
+            __syncwarp();
+            tc_fence_after();
+        }
+        const size_t at = (size_t)(row_first + row) * a.H + h;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 16) {
+            float o[16];
+            if (cnt > 0) tmem_ld16_sync(to + c, o);
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = cnt > 0 ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : 0u;
+            if (real) {
+                uint4 *dst = reinterpret_cast<uint4 *>(b.dv + at * kHeadDim + c);
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
     }
-    if (a.R) for (int c = 0; c < 2; ++c) b.dr_head[((size_t)key * a.H + h) * kSharedDim + c * 32 + lane] = dk[4 + c];
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
 // dr[key] = sum over heads of dr_head[key][h], in fp32 and in head order. 16 keys per block: 16 threads of a
@@ -126,12 +664,30 @@ bool al(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
 cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaStream_t stream)
 {
     const long long tokens = (long long)a.B * a.T, keys = (long long)a.B * a.Tk, rows = tokens * a.H;
+    const long long q_slots = tokens / TL + a.N, k_slots = keys / TL + a.N, v_slots = keys / (2 * TL) + a.N;
+    if (q_slots * a.H > 0x7fffffffLL || k_slots * a.H > 0x7fffffffLL || rows / 8 >= 0x7fffffffLL) return cudaErrorInvalidValue;
+    const int W = kHeadDim + a.R;
+    CUtensorMap q = {}, k = {}, r = {}, v = {}, d = {};          // an empty side's tiles are never copied
+    if (tokens > 0 && (!bf16_heads_map(&q, a.q, W, a.H, tokens, W, (long long)a.H * W, 64, TL) ||
+                       !bf16_heads_map(&d, b.dout, kHeadDim, a.H, tokens, kHeadDim, (long long)a.H * kHeadDim, 64, TL)))
+        return cudaErrorNotSupported;
+    if (keys > 0 && (!bf16_heads_map(&k, a.k, kHeadDim, a.H, keys, a.k_head, a.k_tok, 64, TL) ||
+                     !bf16_heads_map(&v, a.v, kHeadDim, a.H, keys, a.v_head, a.v_tok, 64, TL) ||
+                     (a.R && !bf16_rows_map(&r, a.r, kSharedDim, keys, a.r_tok, 64, TL))))
+        return cudaErrorNotSupported;
+    cudaError_t e;
+    if ((e = cudaFuncSetAttribute(latent_grad_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_END)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(latent_grad_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_END)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(latent_dv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)V_END)) != cudaSuccess)
+        return e;
+    const GradMaps mq = {q, q, d, k, r, v}, mk = {k, r, v, q, q, d};
     if (tokens > 0) {
-        latent_delta_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(a.out, b.dout, b.delta, rows);
-        latent_dq_simple<<<dim3((unsigned)((tokens + 3) / 4), a.H), 128, 0, stream>>>(a, b);
+        latent_stat_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(a.out, b.dout, a.lse, b.stat, tokens, a.H);
+        latent_grad_kernel<true><<<(unsigned)(q_slots * a.H), NT, G_END, stream>>>(a, b, q_slots, mq);
     }
     if (keys > 0) {
-        latent_dkv_simple<<<dim3((unsigned)((keys + 3) / 4), a.H), 128, 0, stream>>>(a, b);
+        latent_grad_kernel<false><<<(unsigned)(k_slots * a.H), NT, G_END, stream>>>(a, b, k_slots, mk);
+        latent_dv_kernel<<<(unsigned)(v_slots * a.H), NT, V_END, stream>>>(a, b, v_slots, mk);
         if (a.R) latent_dr_kernel<<<(unsigned)((keys + 15) / 16), 256, 0, stream>>>(b.dr_head, b.dr, keys, a.H);
     }
     return cudaGetLastError();
@@ -150,7 +706,7 @@ extern "C" {
 size_t kda_latent_bwd_workspace_size(int B, int T, int Tk, int H, int N, int dr)
 {
     if (B < 0 || T < 0 || Tk < 0 || H <= 0 || N < 0 || (dr != 0 && dr != kSharedDim)) return 0;
-    return kStatusBytes + align256((size_t)B * T * H * 4) + align256((size_t)B * Tk * H * dr * 4);
+    return kStatusBytes + align256((size_t)B * T * H * 8) + align256((size_t)B * Tk * H * dr * 4);
 }
 
 kda_status_t kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_shared, const int32_t *cu_seqlens,
@@ -173,8 +729,8 @@ kda_status_t kda_latent_bwd(const void *q, const void *k, const void *v, const v
     LatentBwdArgs b;
     b.dout = (const __nv_bfloat16 *)dout;
     b.dq = (__nv_bfloat16 *)dq; b.dk = (__nv_bfloat16 *)dk_out; b.dv = (__nv_bfloat16 *)dv_out; b.dr = (__nv_bfloat16 *)dk_shared;
-    b.delta = (float *)((unsigned char *)workspace + kStatusBytes);
-    b.dr_head = (float *)((unsigned char *)b.delta + align256((size_t)B * T * H * 4));
+    b.stat = (float *)((unsigned char *)workspace + kStatusBytes);
+    b.dr_head = (float *)((unsigned char *)b.stat + align256((size_t)B * T * H * 8));
     cudaStream_t st = (cudaStream_t)stream;
     if (cudaMemsetAsync(workspace, 0, kStatusBytes, st) != cudaSuccess) return KDA_ERR_CUDA;
     if (N == 0 || B == 0) return KDA_OK;

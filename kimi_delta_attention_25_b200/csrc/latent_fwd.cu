@@ -38,28 +38,6 @@ enum { B_Q, B_FULL, B_EMPTY = B_FULL + NRING, B_S = B_EMPTY + NRING, B_PA = B_S 
        B_DRAIN = B_PV + 2, N_BARS };
 constexpr uint32_t TM_S = 0, TM_O = 256;      // S (and P over it) of the two tiles, O of the two tiles
 
-struct Tile { int n; long long q0, qn, k0, kn; };   // sequence; the block's first query row, rows left, its keys
-
-// Query slot `slot` (256 rows each; slot of sequence n's tile c: floor(first row / 256) + n + c).
-__device__ __forceinline__ bool slot_tile(const LatentArgs &a, long long slot, Tile *t, LatentSpan *s)
-{
-    int lo = 0, hi = a.N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        const long long st = a.cu_q ? (long long)a.cu_q[mid] : (long long)mid * a.T;
-        if (st / (2 * QT) + mid <= slot) lo = mid; else hi = mid - 1;
-    }
-    if (!latent_span(a.cu_q, a.cu_k, lo, a.T, a.Tk, s)) return false;
-    const long long c = slot - (s->q0 / (2 * QT) + lo);
-    if (c < 0 || c * 2 * QT >= s->q1 - s->q0) return false;
-    t->n = lo;
-    t->q0 = s->q0 + c * 2 * QT;
-    t->qn = s->q1 - t->q0;
-    t->k0 = s->k0;
-    t->kn = s->k1 - s->k0;
-    return true;
-}
-
 __global__ void __launch_bounds__(NT, 1)
 latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r)
@@ -74,11 +52,13 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
         check_offsets(a.cu_q, a.N, a.T, a.status);
         check_offsets(a.cu_k, a.N, a.Tk, a.status);
     }
-    Tile t;
+    int n;
     LatentSpan span;
-    if (!slot_tile(a, slot, &t, &span)) return;                        // uniform
-    // tiles of keys that some row of query tile i sees: rows r0 .. of the sequence, row r up to key r + Lk - Lq
-    const long long shift = t.kn - (span.q1 - span.q0), r0 = t.q0 - span.q0;
+    long long r0;                              // the block's first row within its sequence
+    if (!latent_slot(a.cu_q, a, a.T, false, 2 * QT, slot, &n, &span, &r0)) return;   // uniform
+    struct { long long q0, qn, k0, kn; } t = {span.q0 + r0, span.q1 - span.q0 - r0, span.k0, span.k1 - span.k0};
+    // tiles of keys that some row of query tile i sees: row r of the sequence sees keys up to r + Lk - Lq
+    const long long shift = t.kn - (span.q1 - span.q0);
     int nt[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
