@@ -23,7 +23,7 @@ namespace {
 using namespace sm100;
 
 constexpr int TL = 128;                       // rows and columns of a tile
-constexpr int NT = 8 * 32 + 64, W_LOAD = 8, W_MMA = 9;
+constexpr int NT = 8 * 32 + 96, W_LOAD = 8, W_MMA = 9;   // two issuing warps (one takes longer than the tensor cores)
 constexpr uint32_t UNIT = 16384;              // 128 rows x 64 channels, 128-byte swizzle
 constexpr uint32_t SMEM_MAX = 232448;
 
@@ -58,15 +58,14 @@ constexpr uint32_t G_A1 = 0, G_A2 = 3 * UNIT, G_B1 = 5 * UNIT, G_B2 = G_B1 + N1 
                    G_BAR = G_STAT + 2048, G_END = G_BAR + 320;
 static_assert(G_END <= SMEM_MAX, "shared memory");
 enum { G_RES, G_F1, G_E1 = G_F1 + N1, G_F2 = G_E1 + N1, G_E2 = G_F2 + N2, G_S = G_E2 + N2, G_SFREE, G_P, G_PFREE, G_DS,
-       G_ACC, G_DRAIN, G_NBARS };
+       G_ACC, G_DRAIN, G_NBARS = G_DRAIN + 2 };
 static_assert(G_NBARS * 8 + 16 <= 320, "barriers");
 constexpr uint32_t TM_S = 0, TM_P = 128, TM_DS = 256, TM_ACC = 320;
 
 struct GradMaps { CUtensorMap a1, a1r, a2, b1, b1r, b2; };   // dq: q, -, dout, k, r, v; dk: k, r, v, q, -, dout
 
-// S(j + 1), then the accumulating product of tile j, then dP(j + 1): each product's operands are ready by the
-// time its turn comes (dS(j) is formed from dP(j) while S(j + 1) runs), and the units of B1 that the
-// accumulation frees one by one are filled again before S(j + 2) needs them.
+// While dS(j) is formed from dP(j), S(j + 1) runs; while P(j + 1) is formed from it, the accumulating product of
+// tile j and dP(j + 1) do. The units of B1 are freed one by one by the accumulation.
 template <bool DQ>
 __global__ void __launch_bounds__(NT, 1)
 latent_grad_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_constant__ GradMaps maps)
@@ -163,77 +162,73 @@ latent_grad_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_
                 for (int i = max(0, used2 - N2); i < used2; ++i) mbar_wait(&bars[G_F2 + i % N2], (i / N2) & 1, 100000000LL);
             }
         }
-    } else if (warp == W_MMA) {
-        // ======================================================================== MMA issuer
+    } else if (warp >= W_MMA) {
+        // ======================================================================== MMA issuers
+        // The first warp issues S and dP, the second the accumulation; barriers order them where they depend on
+        // one another.
         const bool el = elect_one();
         constexpr uint32_t id_s = idesc_bf16(TL, TL, 0, 0), id_a = idesc_bf16(TL, 64, 0, 1);
         constexpr uint32_t hi = desc_hi(1024, SW_128B);
-        const uint32_t a1_lo = desc_lo(sbase + G_A1, 16), a2_lo = desc_lo(sbase + G_A2, 16);
         const uint32_t b1_lo = desc_lo(sbase + G_B1, 16), b2_lo = desc_lo(sbase + G_B2, 16);
         const int ntu = __reduce_max_sync(0xffffffffu, nt);
-        int s1 = 0, c1 = 0, s2 = 0;             // ring slots: B1 for the scores, B1 for the accumulation, B2
-        uint32_t p1 = 0, p2 = 0;
-        auto scores = [&]() {
-            for (int u = 0; u < u1; ++u) {
-                wait(G_F1 + s1, p1);
+        if (warp == W_MMA) {
+            const uint32_t a1_lo = desc_lo(sbase + G_A1, 16), a2_lo = desc_lo(sbase + G_A2, 16);
+            int s1 = 0, s2 = 0;
+            uint32_t p1 = 0, p2 = 0;
+            if (ntu > 0) wait(G_RES, 0);
+            for (int j = 0; j < ntu; ++j) {
+                if (j > 0) wait(G_SFREE, (j - 1) & 1);
+                for (int u = 0; u < u1; ++u) {
+                    wait(G_F1 + s1, p1);
+                    tc_fence_after();
+                    if (el) {
+                        const uint32_t x = a1_lo + u * (UNIT / 16), y = b1_lo + s1 * (UNIT / 16);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            umma_ss(tmem + TM_S, desc64(x + e * 2, hi), desc64(y + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                    }
+                    if (++s1 == N1) { s1 = 0; p1 ^= 1; }
+                }
+                if (el) umma_commit(&bars[G_S]);
+                if (j > 0) wait(G_PFREE, (j - 1) & 1);
+                for (int u = 0; u < 2; ++u) {
+                    wait(G_F2 + s2, p2);
+                    tc_fence_after();
+                    if (el) {
+                        const uint32_t x = a2_lo + u * (UNIT / 16), y = b2_lo + s2 * (UNIT / 16);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            umma_ss(tmem + TM_P, desc64(x + e * 2, hi), desc64(y + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                        umma_commit(&bars[G_E2 + s2]);
+                    }
+                    if (++s2 == N2) { s2 = 0; p2 ^= 1; }
+                }
+                if (el) umma_commit(&bars[G_P]);
+                if (*abort_flag) break;
+            }
+        } else {
+            int c1 = 0;
+            for (int j = 0; j < ntu; ++j) {
+                wait(G_DS, j & 1);                  // B1 is there: the scores that dS came from read it
                 tc_fence_after();
-                if (el) {
-                    const uint32_t x = a1_lo + u * (UNIT / 16), y = b1_lo + s1 * (UNIT / 16);
+                for (int u = 0; u < u1; ++u) {
+                    if (el) {
+                        const uint32_t y = b1_lo + c1 * (UNIT / 16);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        umma_ss(tmem + TM_S, desc64(x + e * 2, hi), desc64(y + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                        for (int e = 0; e < 8; ++e)
+                            umma_ts(tmem + TM_ACC + u * 64, tmem + TM_DS + e * 8, desc64(y + e * 128, hi), id_a, (e > 0 || j > 0) ? 1 : 0);
+                        umma_commit(&bars[G_E1 + c1]);
+                    }
+                    if (++c1 == N1) c1 = 0;
                 }
-                if (++s1 == N1) { s1 = 0; p1 ^= 1; }
+                if (el) umma_commit(&bars[G_ACC]);
+                if (*abort_flag) break;
             }
-            if (el) umma_commit(&bars[G_S]);
-        };
-        auto dp = [&]() {
-            for (int u = 0; u < 2; ++u) {
-                wait(G_F2 + s2, p2);
-                tc_fence_after();
-                if (el) {
-                    const uint32_t x = a2_lo + u * (UNIT / 16), y = b2_lo + s2 * (UNIT / 16);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        umma_ss(tmem + TM_P, desc64(x + e * 2, hi), desc64(y + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
-                    umma_commit(&bars[G_E2 + s2]);
-                }
-                if (++s2 == N2) { s2 = 0; p2 ^= 1; }
-            }
-            if (el) umma_commit(&bars[G_P]);
-        };
-        if (ntu > 0) {
-            wait(G_RES, 0);
-            scores();
-            dp();
-        }
-        for (int j = 0; j < ntu; ++j) {
-            if (j + 1 < ntu) {
-                wait(G_SFREE, j & 1);
-                scores();
-            }
-            wait(G_DS, j & 1);
-            tc_fence_after();
-            for (int u = 0; u < u1; ++u) {
-                if (el) {
-                    const uint32_t y = b1_lo + c1 * (UNIT / 16);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        umma_ts(tmem + TM_ACC + u * 64, tmem + TM_DS + e * 8, desc64(y + e * 128, hi), id_a, (e > 0 || j > 0) ? 1 : 0);
-                    umma_commit(&bars[G_E1 + c1]);
-                }
-                if (++c1 == N1) c1 = 0;
-            }
-            if (el) umma_commit(&bars[G_ACC]);
-            if (j + 1 < ntu) {
-                wait(G_PFREE, j & 1);
-                dp();
-            }
-            if (*abort_flag) break;
         }
         if (el) {
-            umma_commit(&bars[G_DRAIN]);
-            if (!mbar_wait(&bars[G_DRAIN], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
+            uint64_t *drain = &bars[G_DRAIN + warp - W_MMA];
+            umma_commit(drain);
+            if (!mbar_wait(drain, 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
         }
     } else {
         // ============================================================================ P and dS
@@ -377,7 +372,8 @@ latent_grad_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_
 constexpr int NV = 8;
 constexpr uint32_t V_A = 0, V_RING = 6 * UNIT, V_STAT = V_RING + NV * UNIT, V_BAR = V_STAT + 1024, V_END = V_BAR + 320;
 static_assert(V_END <= SMEM_MAX, "shared memory");
-enum { V_RES, V_F, V_E = V_F + NV, V_S = V_E + NV, V_PA = V_S + 2, V_PB = V_PA + 2, V_PV = V_PB + 2, V_DRAIN = V_PV + 2, V_NBARS };
+enum { V_RES, V_F, V_E = V_F + NV, V_S = V_E + NV, V_PA = V_S + 2, V_PB = V_PA + 2, V_PV = V_PB + 2,
+       V_DRAIN = V_PV + 2, V_NBARS = V_DRAIN + 2 };
 constexpr uint32_t TV_S = 0, TV_O = 256;
 
 __global__ void __launch_bounds__(NT, 1)
@@ -409,7 +405,7 @@ latent_dv_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_co
     volatile int *ctl = reinterpret_cast<volatile int *>(bars + V_NBARS);
     if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
     if (tid == 0) {
-        for (int i = 0; i < V_NBARS; ++i) mbar_init(&bars[i], (i >= V_PA && i < V_PV) ? 4 : 1);
+        for (int i = 0; i < V_NBARS; ++i) mbar_init(&bars[i], (i >= V_PA && i < V_PV) ? 4 : (i >= V_E && i < V_S) ? 2 : 1);
         ctl[1] = 0;
         fence_mbar_init();
     }
@@ -458,87 +454,69 @@ latent_dv_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_co
                 for (int i = max(0, used - NV); i < used; ++i) mbar_wait(&bars[V_F + i % NV], (i / NV) & 1, 100000000LL);
             }
         }
-    } else if (warp == W_MMA) {
-        // ======================================================================== MMA issuer
+    } else if (warp >= W_MMA) {
+        // ======================================================================== MMA issuers, one per key tile
         const bool el = elect_one();
+        const int i = warp - W_MMA;
         constexpr uint32_t id_s = idesc_bf16(TL, TL, 0, 0), id_o = idesc_bf16(TL, 64, 0, 1);
         constexpr uint32_t hi = desc_hi(1024, SW_128B);
-        const uint32_t a_lo = desc_lo(sbase + V_A, 16), r_lo = desc_lo(sbase + V_RING, 16);
-        const int ntu = __reduce_max_sync(0xffffffffu, nt);
-        const int f0 = __reduce_max_sync(0xffffffffu, first[0] - t_lo), f1 = __reduce_max_sync(0xffffffffu, first[1] - t_lo);
-        int s = 0, qs = 0, os = 0;
+        const uint32_t a_lo = desc_lo(sbase + V_A + i * 3 * UNIT, 16), r_lo = desc_lo(sbase + V_RING, 16);
+        const uint32_t d_s = tmem + TV_S + i * 128, d_o = tmem + TV_O + i * 128;
+        const int ntu = __reduce_max_sync(0xffffffffu, nt), f = __reduce_max_sync(0xffffffffu, first[i] - t_lo);
+        int s = 0;
         uint32_t ph = 0;
-        auto advance = [&](int x) { return x + 1 == NV ? 0 : x + 1; };
-        auto take = [&](int count) {
-            for (int u = 0; u < count; ++u) {
+        auto scores = [&](bool mine) {
+            for (int u = 0; u < u1; ++u) {
                 wait(V_F + s, ph);
+                if (el) {
+                    if (mine) {
+                        tc_fence_after();
+                        const uint32_t k = a_lo + u * (UNIT / 16), q = r_lo + s * (UNIT / 16);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            umma_ss(d_s, desc64(k + e * 2, hi), desc64(q + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                    }
+                    umma_commit(&bars[V_E + s]);
+                }
                 if (++s == NV) { s = 0; ph ^= 1; }
             }
-            tc_fence_after();
-        };
-        auto scores = [&](int i) {
-            int x = qs;
-            for (int u = 0; u < u1; ++u) {
-                if (el) {
-                    const uint32_t k = a_lo + (i * 3 + u) * (UNIT / 16), q = r_lo + x * (UNIT / 16);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        umma_ss(tmem + TV_S + i * 128, desc64(k + e * 2, hi), desc64(q + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
-                }
-                x = advance(x);
-            }
-            if (el) umma_commit(&bars[V_S + i]);
-        };
-        auto release = [&](int x, int count) {
-            for (int u = 0; u < count; ++u) {
-                if (el) umma_commit(&bars[V_E + x]);
-                x = advance(x);
-            }
+            if (el && mine) umma_commit(&bars[V_S + i]);
         };
         if (ntu > 0) {
             wait(V_RES, 0);
-            qs = s;
-            take(u1);
-            if (f0 == 0) scores(0);
-            if (f1 == 0) scores(1);
-            release(qs, u1);
+            scores(f == 0);
         }
         for (int j = 0; j < ntu; ++j) {
-            os = s;
-            take(2);
-            const bool more = j + 1 < ntu;
-            if (more) qs = s;
+            const int s0 = s;
+            wait(V_F + s, ph);
+            if (++s == NV) { s = 0; ph ^= 1; }
+            const int s1 = s;
+            wait(V_F + s, ph);
+            if (++s == NV) { s = 0; ph ^= 1; }
+            if (j >= f) {
+                const uint32_t v0 = r_lo + s0 * (UNIT / 16), v1 = r_lo + s1 * (UNIT / 16);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int f = i ? f1 : f0;
-                if (j >= f) {
-                    const uint32_t d = tmem + TV_O + i * 128, p = tmem + TV_S + i * 128;
-                    const uint32_t v0 = r_lo + os * (UNIT / 16), v1 = r_lo + advance(os) * (UNIT / 16);
+                for (int half = 0; half < 2; ++half) {
+                    wait((half ? V_PB : V_PA) + i, (j - f) & 1);
+                    tc_fence_after();
+                    if (el) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        wait((half ? V_PB : V_PA) + i, (j - f) & 1);
-                        tc_fence_after();
-                        if (el) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t acc = (half > 0 || e > 0 || j > f) ? 1 : 0, step = (half * 4 + e) * 128;
-                                umma_ts(d, p + (half * 4 + e) * 8, desc64(v0 + step, hi), id_o, acc);
-                                umma_ts(d + 64, p + (half * 4 + e) * 8, desc64(v1 + step, hi), id_o, acc);
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t acc = (half > 0 || e > 0 || j > f) ? 1 : 0, step = (half * 4 + e) * 128;
+                            umma_ts(d_o, d_s + (half * 4 + e) * 8, desc64(v0 + step, hi), id_o, acc);
+                            umma_ts(d_o + 64, d_s + (half * 4 + e) * 8, desc64(v1 + step, hi), id_o, acc);
                         }
                     }
-                    if (el) umma_commit(&bars[V_PV + i]);
                 }
-                if (i == 0 && more) take(u1);
-                if (i == 1) release(os, 2);
-                if (more && j + 1 >= f) scores(i);
+                if (el) umma_commit(&bars[V_PV + i]);
             }
-            if (more) release(qs, u1);
+            if (el) { umma_commit(&bars[V_E + s0]); umma_commit(&bars[V_E + s1]); }
+            if (j + 1 < ntu) scores(j + 1 >= f);
             if (*abort_flag) break;
         }
         if (el) {
-            umma_commit(&bars[V_DRAIN]);
-            if (!mbar_wait(&bars[V_DRAIN], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
+            umma_commit(&bars[V_DRAIN + i]);
+            if (!mbar_wait(&bars[V_DRAIN + i], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
         }
     } else {
         // ============================================================================ P

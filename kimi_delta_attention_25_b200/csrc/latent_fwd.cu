@@ -15,8 +15,9 @@
 //    that O is rarely rescaled; the same threads do it.
 //  - P is handed over in two halves, and the second product starts on the first while the second's
 //    exponentials are being taken.
-//  - Keys and values stream through a ring of eight 16 KB units (128 rows x 64 channels), each freed by the
-//    product that used it last; the shared key part is the third unit of every key tile.
+//  - The issuing and loading warps share their schedulers with the warps that take exponentials, which leave
+//    them few slots: their loops are kept short (one barrier per tile of keys or values, the widest products),
+//    and warp-uniform with one issuing thread, so that descriptors stay in uniform registers.
 // Blocks start with the last query tiles, which see the most keys under the causal mask. P's rounding to bf16
 // is the operand type's; sums and statistics are fp32.
 #include "latent.cuh"
@@ -30,11 +31,10 @@ using namespace sm100;
 constexpr int QT = 128, KT = 128;             // query rows of a tile (two per block), keys of a tile
 constexpr int NT = 8 * 32 + 64, W_LOAD = 8, W_MMA = 9;
 constexpr uint32_t UNIT = 16384;              // 128 rows x 64 channels, 128-byte swizzle
-constexpr int NRING = 8;
-constexpr uint32_t OFF_Q = 0, OFF_RING = 6 * UNIT, OFF_BAR = OFF_RING + NRING * UNIT;
+constexpr uint32_t OFF_Q = 0, OFF_K = 6 * UNIT, OFF_V = OFF_K + 6 * UNIT, OFF_BAR = OFF_V + 2 * UNIT;   // two tiles of Q, two of K, one of V
 constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
 static_assert(SMEM <= 232448, "shared memory");
-enum { B_Q, B_FULL, B_EMPTY = B_FULL + NRING, B_S = B_EMPTY + NRING, B_PA = B_S + 2, B_PB = B_PA + 2, B_PV = B_PB + 2,
+enum { B_Q, B_KF, B_KE = B_KF + 2, B_VF = B_KE + 2, B_VE, B_S, B_P = B_S + 2, B_PV = B_P + 2,
        B_DRAIN = B_PV + 2, N_BARS };
 constexpr uint32_t TM_S = 0, TM_O = 256;      // S (and P over it) of the two tiles, O of the two tiles
 
@@ -74,11 +74,13 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
     if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
     if (tid == 0) {
         mbar_init(&bars[B_Q], 1);
-        for (int i = 0; i < NRING; ++i) { mbar_init(&bars[B_FULL + i], 1); mbar_init(&bars[B_EMPTY + i], 1); }
+        mbar_init(&bars[B_VF], 1);
+        mbar_init(&bars[B_VE], 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars[B_KF + i], 1);
+            mbar_init(&bars[B_KE + i], 1);
             mbar_init(&bars[B_S + i], 1);
-            mbar_init(&bars[B_PA + i], 4);
-            mbar_init(&bars[B_PB + i], 4);
+            mbar_init(&bars[B_P + i], 4);
             mbar_init(&bars[B_PV + i], 1);
         }
         mbar_init(&bars[B_DRAIN], 1);
@@ -109,107 +111,83 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
             for (int i = 0; i < 2; ++i)
                 for (int u = 0; u < kunits; ++u)
                     tma_load_3d(sm + OFF_Q + (i * 3 + u) * UNIT, &tm_q, &bars[B_Q], u * 64, (int)(t.q0 + i * QT), h);
-            int s = 0, used = 0;
-            uint32_t ph = 0;
             bool ok = true;
-            auto unit = [&](const CUtensorMap *m, int c, int row, bool shared) {
-                if (used >= NRING) ok = wait(B_EMPTY + s, ph ^ 1);
-                if (!ok) return;
-                mbar_arrive_expect_tx(&bars[B_FULL + s], UNIT);
-                if (shared) tma_load_2d(sm + OFF_RING + s * UNIT, m, &bars[B_FULL + s], c, row);
-                else tma_load_3d(sm + OFF_RING + s * UNIT, m, &bars[B_FULL + s], c, row, h);
-                ++used;
-                if (++s == NRING) { s = 0; ph ^= 1; }
-            };
-            for (int j = 0; j < ntile && ok; ++j) {
-                const int row = (int)(t.k0 + (long long)j * KT);
-                for (int u = 0; u < 2 && ok; ++u) unit(&tm_k, u * 64, row, false);
-                if (a.R && ok) unit(&tm_r, 0, row, true);
-                for (int u = 0; u < 2 && ok; ++u) unit(&tm_v, u * 64, row, false);
+            int j = 0;
+            for (; j < ntile; ++j) {
+                const int row = (int)(t.k0 + (long long)j * KT), b = j & 1;
+                unsigned char *kd = sm + OFF_K + b * 3 * UNIT;
+                if (j >= 2 && !(ok = wait(B_KE + b, ((j >> 1) - 1) & 1))) break;
+                mbar_arrive_expect_tx(&bars[B_KF + b], kunits * UNIT);
+                tma_load_3d(kd, &tm_k, &bars[B_KF + b], 0, row, h);
+                tma_load_3d(kd + UNIT, &tm_k, &bars[B_KF + b], 64, row, h);
+                if (a.R) tma_load_2d(kd + 2 * UNIT, &tm_r, &bars[B_KF + b], 0, row);
+                if (j >= 1 && !(ok = wait(B_VE, (j - 1) & 1))) break;
+                mbar_arrive_expect_tx(&bars[B_VF], 2 * UNIT);
+                tma_load_3d(sm + OFF_V, &tm_v, &bars[B_VF], 0, row, h);
+                tma_load_3d(sm + OFF_V + UNIT, &tm_v, &bars[B_VF], 64, row, h);
             }
             if (!ok) {                          // a wait ran out: what is in flight lands before the block ends
                 mbar_wait(&bars[B_Q], 0, 100000000LL);
-                for (int i = max(0, used - NRING); i < used; ++i) mbar_wait(&bars[B_FULL + i % NRING], (i / NRING) & 1, 100000000LL);
+                for (int x = max(0, j - 1); x <= j && x < ntile; ++x) mbar_wait(&bars[B_KF + (x & 1)], (x >> 1) & 1, 100000000LL);
+                if (j > 0) mbar_wait(&bars[B_VF], (j - 1) & 1, 100000000LL);
             }
         }
     } else if (warp == W_MMA) {
         // ======================================================================== MMA issuer
         // The whole warp runs the loop and one thread issues: slots and addresses stay warp-uniform.
         const bool el = elect_one();
-        constexpr uint32_t id_s = idesc_bf16(QT, KT, 0, 0), id_o = idesc_bf16(QT, 64, 0, 1);
+        constexpr uint32_t id_s = idesc_bf16(QT, KT, 0, 0), id_o = idesc_bf16(QT, 128, 0, 1);
         constexpr uint32_t hi = desc_hi(1024, SW_128B);
-        const uint32_t q_lo = desc_lo(sbase + OFF_Q, 16), k_lo = desc_lo(sbase + OFF_RING, 16);
+        const uint32_t q_lo = desc_lo(sbase + OFF_Q, 16), k_lo = desc_lo(sbase + OFF_K, 16), v_lo = desc_lo(sbase + OFF_V, UNIT);
         const int nt0 = __reduce_max_sync(0xffffffffu, nt[0]), nt1 = __reduce_max_sync(0xffffffffu, nt[1]);
         const int ntu = max(nt0, nt1);
-        int s = 0, ks = 0, vs = 0;              // ring slot of the next unit; of this tile's keys and values
-        uint32_t ph = 0;
-        auto advance = [&](int x) { return x + 1 == NRING ? 0 : x + 1; };
-        auto take = [&](int count) {            // waits for the next `count` units
-            for (int u = 0; u < count; ++u) {
-                wait(B_FULL + s, ph);
-                if (++s == NRING) { s = 0; ph ^= 1; }
-            }
-            tc_fence_after();
-        };
-        auto scores = [&](int i) {
-            int x = ks;
-            for (int u = 0; u < kunits; ++u) {
-                if (el) {
-                    const uint32_t q = q_lo + (i * 3 + u) * (UNIT / 16), k = k_lo + x * (UNIT / 16);
+        const bool has_r = a.R != 0;
+        auto scores = [&](int i, int b) {
+            if (el) {
+                const uint32_t q = q_lo + i * (3 * UNIT / 16), k = k_lo + b * (3 * UNIT / 16), d = tmem + TM_S + i * 128;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        umma_ss(tmem + TM_S + i * 128, desc64(q + e * 2, hi), desc64(k + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                for (int e = 0; e < 8; ++e)
+                    umma_ss(d, desc64(q + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), desc64(k + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), id_s, e > 0 ? 1 : 0);
+                if (has_r) {
+#pragma unroll
+                    for (int e = 8; e < 12; ++e)
+                        umma_ss(d, desc64(q + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), desc64(k + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), id_s, 1);
                 }
-                x = advance(x);
-            }
-            if (el) umma_commit(&bars[B_S + i]);
-        };
-        auto release = [&](int x, int count) {
-            for (int u = 0; u < count; ++u) {
-                if (el) umma_commit(&bars[B_EMPTY + x]);
-                x = advance(x);
+                umma_commit(&bars[B_S + i]);
             }
         };
         if (ntu > 0) {
             wait(B_Q, 0);
-            ks = s;
-            take(kunits);
-            if (nt0 > 0) scores(0);
-            if (nt1 > 0) scores(1);
-            release(ks, kunits);
+            wait(B_KF, 0);
+            tc_fence_after();
+            if (nt0 > 0) scores(0, 0);
+            if (nt1 > 0) scores(1, 0);
+            if (el) umma_commit(&bars[B_KE]);
         }
         for (int j = 0; j < ntu; ++j) {
-            vs = s;
-            take(2);
+            const int b = (j + 1) & 1;
             const bool more = j + 1 < ntu;
-            if (more) ks = s;
+            wait(B_VF, j & 1);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int nti = i ? nt1 : nt0;
                 if (j < nti) {
-                    // O_i += P_i V, the first 64 keys and then the others, 64 channels at a time
+                    // O_i += P_i V
                     const uint32_t d = tmem + TM_O + i * 128, p = tmem + TM_S + i * 128;
-                    const uint32_t v0 = k_lo + vs * (UNIT / 16), v1 = k_lo + advance(vs) * (UNIT / 16);
+                    wait(B_P + i, j & 1);
+                    tc_fence_after();
+                    if (el) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        wait(half ? B_PB + i : B_PA + i, j & 1);
-                        tc_fence_after();
-                        if (el) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint32_t acc = (half > 0 || e > 0 || j > 0) ? 1 : 0, step = (half * 4 + e) * 128;
-                                umma_ts(d, p + (half * 4 + e) * 8, desc64(v0 + step, hi), id_o, acc);
-                                umma_ts(d + 64, p + (half * 4 + e) * 8, desc64(v1 + step, hi), id_o, acc);
-                            }
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            umma_ts(d, p + e * 8, desc64(v_lo + e * 128, hi), id_o, (e > 0 || j > 0) ? 1 : 0);
+                        umma_commit(&bars[B_PV + i]);
                     }
-                    if (el) umma_commit(&bars[B_PV + i]);
                 }
-                if (i == 0 && more) take(kunits);
-                if (i == 1) release(vs, 2);
-                if (j + 1 < nti) scores(i);
+                if (i == 1 && el) umma_commit(&bars[B_VE]);
+                if (i == 0 && more) { wait(B_KF + b, ((j + 1) >> 1) & 1); tc_fence_after(); }
+                if (j + 1 < nti) scores(i, b);
             }
-            if (more) release(ks, kunits);
+            if (more && el) umma_commit(&bars[B_KE + b]);
             if (*abort_flag) break;
         }
         if (el) {
@@ -233,20 +211,49 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
             wait(B_S + i, j & 1);
             __syncwarp();
             tc_fence_after();
-            float s[128];
-            tmem_ld64_sync(ts, *reinterpret_cast<float (*)[64]>(s));
-            tmem_ld64_sync(ts + 64, *reinterpret_cast<float (*)[64]>(s + 64));
             const int kb = j * KT;
-            if (kb + KT > lim_warp) {
+            const bool edge = kb + KT > lim_warp;
+            // P with the maximum of the tiles before; l gets its sums in pairs
+            const uint64_t sc2 = f2(sc, sc);
+            uint32_t w[64];
+            float sum;
+            auto exps = [&]() {
+                const uint64_t m2 = f2(-m, -m);
+                uint64_t sum2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-                for (int e = 0; e < 128; ++e) s[e] = kb + e < lim ? s[e] : -INFINITY;
-            }
-            float top[4] = {s[0], s[1], s[2], s[3]};
+                for (int c = 0; c < 2; ++c) {
+                    float s[64];
+                    tmem_ld64_sync(ts + c * 64, s);
+                    if (edge) {
 #pragma unroll
-            for (int e = 4; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], s[e]);
-            const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
-            if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-                const float up = fmaxf(m, mx), f = up == m ? 1.f : ex2(m - up);
+                        for (int e = 0; e < 64; ++e) s[e] = kb + c * 64 + e < lim ? s[e] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float x0, x1;
+                        f2_split(f2_fma(f2(s[2 * e], s[2 * e + 1]), sc2, m2), x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        sum2[e & 1] = f2_add(sum2[e & 1], f2(p0, p1));
+                        w[c * 32 + e] = pack_bf16x2(p0, p1);
+                    }
+                }
+                float s0, s1;
+                f2_split(f2_add(sum2[0], sum2[1]), s0, s1);
+                return s0 + s1;
+            };
+            sum = exps();
+            // A sum that large (or none: no maximum yet, or a score that is not finite) means that some score is far
+            // above the maximum. Few tiles come here: the row's maximum, O and l scaled to it, and P again.
+            if (__any_sync(0xffffffffu, !(sum < 32768.f))) {
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 16) {
+                    float s[16];
+                    tmem_ld16_sync(ts + c, s);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) top = fmaxf(top, kb + c + e < lim ? s[e] : -INFINITY);
+                }
+                const float up = fmaxf(m, top * sc), f = up == m ? 1.f : ex2(m - up);
                 m = up;
                 l *= f;
                 if (j > 0) {
@@ -263,48 +270,31 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
                     }
                     tmem_st_wait();
                 }
+                sum = exps();
             }
+            l += sum;
             // values behind the sequence's last key may be anything: zeros, before the second product reads them
             if (kb + KT > t.kn) {
-                const int valid = (int)(t.kn - kb), per = kunits + 2;
-                for (int u = 0; u < 2; ++u) {
-                    const int x = j * per + kunits + u;
-                    wait(B_FULL + x % NRING, (x / NRING) & 1);
-                    unsigned char *un = sm + OFF_RING + (x % NRING) * UNIT;
+                const int valid = (int)(t.kn - kb);
+                wait(B_VF, j & 1);
+                for (int u = 0; u < 2; ++u)
                     for (int e = quad * 32 + lane; e < (KT - valid) * 8; e += 128)
-                        *reinterpret_cast<uint4 *>(un + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
-                }
+                        *reinterpret_cast<uint4 *>(sm + OFF_V + u * UNIT + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int x = half * 64 + c * 32 + 2 * e;
-                        const float p0 = ex2(s[x] * sc - m), p1 = ex2(s[x + 1] * sc - m);
-                        sum[(2 * e) & 3] += p0;
-                        sum[(2 * e + 1) & 3] += p1;
-                        w[e] = pack_bf16x2(p0, p1);
-                    }
-                    tmem_st16u(ts + half * 32 + c * 16, w);
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[(half ? B_PB : B_PA) + i]);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st32(ts, *reinterpret_cast<uint32_t (*)[32]>(w));          // over S, which is read
+            tmem_st32(ts + 32, *reinterpret_cast<uint32_t (*)[32]>(w + 32));
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[B_P + i]);
         }
-        const size_t orow = (size_t)(t.q0 + row) * a.H + h;
         if (nti > 0) {
             wait(B_PV + i, (nti - 1) & 1);
             __syncwarp();
             tc_fence_after();
         }
+        const size_t orow = (size_t)(t.q0 + row) * a.H + h;
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int c = 0; c < 128; c += 16) {
