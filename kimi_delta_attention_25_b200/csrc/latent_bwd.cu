@@ -2,11 +2,11 @@
 // from the forward's lse:  P = exp(s - lse),  D_i = do_i . o_i,  dP = do v^T,  dS = P (dP - D),
 //   dq = scale dS [k, r],  dk = scale dS^T q[:128],  dr = scale sum_h dS^T q[128:],  dv = P^T do.
 //
-// Three kernels, each for one row of tiles, none of them adding to memory that another block adds to:
+// Three kinds of blocks, each for one row of tiles, none of them adding to memory that another block adds to:
 //   dq: rows of 128 queries, over key tiles:    S = Q [K, R]^T, dP = dO V^T,     dq += dS [K, R]
 //   dk: rows of 128 keys, over query tiles:     S^T = [K, R] Q^T, dP^T = V dO^T, dk += dS^T Q
 //   dv: rows of 2 x 128 keys, over query tiles: S^T, dv += P^T dO
-// (the first two are one template: resident operands A1, A2 and streamed ones B1, B2 swap roles). One kernel
+// (the first two are one template: resident operands A1, A2 and streamed ones B1, B2 swap roles). One block
 // for dk and dv would need S^T, dP^T, dk (192 columns) and dv in tensor memory: 576 of 512 columns; with query
 // tiles of 64, which fit, the products over 64 columns read their 128-row operand from shared memory twice as
 // often and cost as much as computing S^T again. A fused dq would need atomic sums or 2 bytes of dS per pair in
@@ -27,26 +27,40 @@ constexpr int NT = 8 * 32 + 96, W_LOAD = 8, W_MMA = 9;   // two issuing warps (o
 constexpr uint32_t UNIT = 16384;              // 128 rows x 64 channels, 128-byte swizzle
 constexpr uint32_t SMEM_MAX = 232448;
 
-// lse in the log2 domain and D_i = do_i . o_i as [H][tokens] (the dk and dv kernels read them along the
-// tokens), one warp per (token, head).
+// lse in the log2 domain and D_i = do_i . o_i as [H][tokens] (the dk and dv blocks read them along the
+// tokens): one warp per head and 32 tokens, half a warp to a row.
 __global__ void __launch_bounds__(256) latent_stat_kernel(const __nv_bfloat16 *__restrict__ out, const __nv_bfloat16 *__restrict__ dout,
                                                           const float *__restrict__ lse, float *__restrict__ stat, long long tokens, int H)
 {
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= tokens * H) return;
-    const uint2 o = reinterpret_cast<const uint2 *>(out + row * kHeadDim)[lane], d = reinterpret_cast<const uint2 *>(dout + row * kHeadDim)[lane];
-    float s = __uint_as_float(o.x << 16) * __uint_as_float(d.x << 16);
-    s += __uint_as_float(o.x & 0xFFFF0000u) * __uint_as_float(d.x & 0xFFFF0000u);
-    s += __uint_as_float(o.y << 16) * __uint_as_float(d.y << 16);
-    s += __uint_as_float(o.y & 0xFFFF0000u) * __uint_as_float(d.y & 0xFFFF0000u);
+    const long long warp = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, h = (int)(warp % H);
+    const long long t0 = warp / H * 32;
+    if (t0 >= tokens) return;
+    float mine = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < 16; ++i) {
+        const long long t = t0 + 2 * i + (lane >> 4);
+        float s = 0.f;
+        if (t < tokens) {
+            const uint4 o = reinterpret_cast<const uint4 *>(out + (t * H + h) * kHeadDim)[lane & 15];
+            const uint4 d = reinterpret_cast<const uint4 *>(dout + (t * H + h) * kHeadDim)[lane & 15];
+            const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, dw[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    if (lane == 0) {
-        const long long at = (row % H) * tokens + row / H;
-        const float l = lse[row];
-        stat[at] = l == -INFINITY ? INFINITY : l * 1.44269504088896341f;
-        stat[tokens * H + at] = s;
+            for (int e = 0; e < 4; ++e) {
+                s += __uint_as_float(ow[e] << 16) * __uint_as_float(dw[e] << 16);
+                s += __uint_as_float(ow[e] & 0xFFFF0000u) * __uint_as_float(dw[e] & 0xFFFF0000u);
+            }
+        }
+#pragma unroll
+        for (int m = 8; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+        const float even = __shfl_sync(0xffffffffu, s, 0), odd = __shfl_sync(0xffffffffu, s, 16);
+        if (lane == 2 * i) mine = even;
+        if (lane == 2 * i + 1) mine = odd;
+    }
+    if (t0 + lane < tokens) {
+        const float l = lse[(t0 + lane) * H + h];
+        stat[h * tokens + t0 + lane] = l == -INFINITY ? INFINITY : l * 1.44269504088896341f;
+        stat[tokens * H + h * tokens + t0 + lane] = mine;
     }
 }
 
@@ -67,19 +81,11 @@ struct GradMaps { CUtensorMap a1, a1r, a2, b1, b1r, b2; };   // dq: q, -, dout, 
 // While dS(j) is formed from dP(j), S(j + 1) runs; while P(j + 1) is formed from it, the accumulating product of
 // tile j and dP(j + 1) do. The units of B1 are freed one by one by the accumulation.
 template <bool DQ>
-__global__ void __launch_bounds__(NT, 1)
-latent_grad_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_constant__ GradMaps maps)
+__device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdArgs &b, long long slot, int h, const GradMaps &maps,
+                                           unsigned char *sm)
 {
-    extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.H;
-    const long long slot = DQ ? slots - 1 - blockIdx.x / a.H : blockIdx.x / a.H;   // the longest rows of tiles first
-    if (blockIdx.x == 0) {
-        check_offsets(a.cu_q, a.N, a.T, a.status);
-        check_offsets(a.cu_k, a.N, a.Tk, a.status);
-    }
-    if (sbase & 1023u) { if (tid == 0) set_status(a.status, KDA_ERR_CUDA); return; }   // the swizzle needs it (it holds)
     int n;
     LatentSpan sp;
     long long r0;
@@ -369,25 +375,22 @@ latent_grad_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_
 // ------------------------------------------------------------------------------------------ dv
 // The forward kernel's structure with the roles of queries and keys exchanged and lse known: two key tiles at
 // once, P^T over S^T's columns as the A operand of dv += P^T dO.
-constexpr int NV = 8;
-constexpr uint32_t V_A = 0, V_RING = 6 * UNIT, V_STAT = V_RING + NV * UNIT, V_BAR = V_STAT + 1024, V_END = V_BAR + 320;
+constexpr int NVQ = 4;                        // ring of query units; dO has two tiles
+constexpr uint32_t V_A = 0, V_Q = 6 * UNIT, V_D = V_Q + NVQ * UNIT, V_STAT = V_D + 4 * UNIT, V_BAR = V_STAT + 1024, V_END = V_BAR + 320;
 static_assert(V_END <= SMEM_MAX, "shared memory");
-enum { V_RES, V_F, V_E = V_F + NV, V_S = V_E + NV, V_PA = V_S + 2, V_PB = V_PA + 2, V_PV = V_PB + 2,
-       V_DRAIN = V_PV + 2, V_NBARS = V_DRAIN + 2 };
+enum { V_RES, V_QF, V_QE = V_QF + NVQ, V_DF = V_QE + NVQ, V_DE = V_DF + 2, V_S = V_DE + 2, V_PA = V_S + 2, V_PB = V_PA + 2, V_PV = V_PB + 2,
+       V_DRAIN = V_PV + 2, V_NBARS };
 constexpr uint32_t TV_S = 0, TV_O = 256;
 
-__global__ void __launch_bounds__(NT, 1)
-latent_dv_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_constant__ GradMaps maps)
+__device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArgs &b, long long slot, int h, const GradMaps &maps,
+                                         unsigned char *sm)
 {
-    extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x % a.H;
-    if (sbase & 1023u) { if (tid == 0) set_status(a.status, KDA_ERR_CUDA); return; }
     int n;
     LatentSpan sp;
     long long r0;
-    if (!latent_slot(a.cu_k, a, a.Tk, true, 2 * TL, blockIdx.x / a.H, &n, &sp, &r0)) return;   // uniform
+    if (!latent_slot(a.cu_k, a, a.Tk, true, 2 * TL, slot, &n, &sp, &r0)) return;   // uniform
     const long long Lq = sp.q1 - sp.q0, Lk = sp.k1 - sp.k0, shift = Lk - Lq, rows = Lk - r0;
     const long long row_first = sp.k0 + r0;
     // query tiles that see some key of tile i: from the first that sees its first key to the last
@@ -405,7 +408,7 @@ latent_dv_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_co
     volatile int *ctl = reinterpret_cast<volatile int *>(bars + V_NBARS);
     if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
     if (tid == 0) {
-        for (int i = 0; i < V_NBARS; ++i) mbar_init(&bars[i], (i >= V_PA && i < V_PV) ? 4 : (i >= V_E && i < V_S) ? 2 : 1);
+        for (int i = 0; i < V_NBARS; ++i) mbar_init(&bars[i], (i >= V_PA && i < V_PV) ? 4 : 1);
         ctl[1] = 0;
         fence_mbar_init();
     }
@@ -435,90 +438,94 @@ latent_dv_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_co
                     if (u == 2) tma_load_2d(dst, &maps.a1r, &bars[V_RES], 0, (int)(row_first + i * TL));
                     else tma_load_3d(dst, &maps.a1, &bars[V_RES], u * 64, (int)(row_first + i * TL), h);
                 }
-            int s = 0, used = 0;
+            int s = 0, used = 0, j = 0;
             uint32_t ph = 0;
             bool ok = true;
-            for (int j = 0; j < nt && ok; ++j) {
-                const int row = (int)(sp.q0 + (long long)(t_lo + j) * TL);
-                for (int u = 0; u < u1 + 2 && ok; ++u) {
-                    if (used >= NV) ok = wait(V_E + s, ph ^ 1);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&bars[V_F + s], UNIT);
-                    tma_load_3d(sm + V_RING + s * UNIT, u < u1 ? &maps.b1 : &maps.b2, &bars[V_F + s], (u < u1 ? u : u - u1) * 64, row, h);
+            for (; j < nt; ++j) {
+                const int row = (int)(sp.q0 + (long long)(t_lo + j) * TL), b = j & 1;
+                for (int u = 0; u < u1; ++u) {
+                    if (used >= NVQ && !(ok = wait(V_QE + s, ph ^ 1))) break;
+                    mbar_arrive_expect_tx(&bars[V_QF + s], UNIT);
+                    tma_load_3d(sm + V_Q + s * UNIT, &maps.b1, &bars[V_QF + s], u * 64, row, h);
                     ++used;
-                    if (++s == NV) { s = 0; ph ^= 1; }
+                    if (++s == NVQ) { s = 0; ph ^= 1; }
                 }
+                if (!ok || (j >= 2 && !(ok = wait(V_DE + b, ((j >> 1) - 1) & 1)))) break;
+                unsigned char *dst = sm + V_D + b * 2 * UNIT;
+                mbar_arrive_expect_tx(&bars[V_DF + b], 2 * UNIT);
+                tma_load_3d(dst, &maps.b2, &bars[V_DF + b], 0, row, h);
+                tma_load_3d(dst + UNIT, &maps.b2, &bars[V_DF + b], 64, row, h);
             }
             if (!ok) {
                 mbar_wait(&bars[V_RES], 0, 100000000LL);
-                for (int i = max(0, used - NV); i < used; ++i) mbar_wait(&bars[V_F + i % NV], (i / NV) & 1, 100000000LL);
+                for (int x = max(0, used - NVQ); x < used; ++x) mbar_wait(&bars[V_QF + x % NVQ], (x / NVQ) & 1, 100000000LL);
+                for (int x = max(0, j - 2); x < j; ++x) mbar_wait(&bars[V_DF + (x & 1)], (x >> 1) & 1, 100000000LL);
             }
         }
-    } else if (warp >= W_MMA) {
-        // ======================================================================== MMA issuers, one per key tile
+    } else if (warp == W_MMA) {
+        // ======================================================================== MMA issuer, as in the forward kernel
         const bool el = elect_one();
-        const int i = warp - W_MMA;
-        constexpr uint32_t id_s = idesc_bf16(TL, TL, 0, 0), id_o = idesc_bf16(TL, 64, 0, 1);
+        constexpr uint32_t id_s = idesc_bf16(TL, TL, 0, 0), id_o = idesc_bf16(TL, 128, 0, 1);
         constexpr uint32_t hi = desc_hi(1024, SW_128B);
-        const uint32_t a_lo = desc_lo(sbase + V_A + i * 3 * UNIT, 16), r_lo = desc_lo(sbase + V_RING, 16);
-        const uint32_t d_s = tmem + TV_S + i * 128, d_o = tmem + TV_O + i * 128;
-        const int ntu = __reduce_max_sync(0xffffffffu, nt), f = __reduce_max_sync(0xffffffffu, first[i] - t_lo);
-        int s = 0;
-        uint32_t ph = 0;
-        auto scores = [&](bool mine) {
+        const uint32_t a_lo = desc_lo(sbase + V_A, 16), q_lo = desc_lo(sbase + V_Q, 16), d_lo = desc_lo(sbase + V_D, UNIT);
+        const int ntu = __reduce_max_sync(0xffffffffu, nt);
+        const int f0 = __reduce_max_sync(0xffffffffu, first[0] - t_lo), f1 = __reduce_max_sync(0xffffffffu, first[1] - t_lo);
+        int qs = 0;
+        uint32_t qp = 0;
+        auto scores = [&](int i, bool mine) {
+            int x = qs;
+            uint32_t ph = qp;
             for (int u = 0; u < u1; ++u) {
-                wait(V_F + s, ph);
+                if (i == 0) { wait(V_QF + x, ph); tc_fence_after(); }
                 if (el) {
                     if (mine) {
-                        tc_fence_after();
-                        const uint32_t k = a_lo + u * (UNIT / 16), q = r_lo + s * (UNIT / 16);
+                        const uint32_t k = a_lo + (i * 3 + u) * (UNIT / 16), q = q_lo + x * (UNIT / 16), d = tmem + TV_S + i * 128;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            umma_ss(d_s, desc64(k + e * 2, hi), desc64(q + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                        for (int e = 0; e < 4; ++e) umma_ss(d, desc64(k + e * 2, hi), desc64(q + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
                     }
-                    umma_commit(&bars[V_E + s]);
+                    if (i == 1) umma_commit(&bars[V_QE + x]);
                 }
-                if (++s == NV) { s = 0; ph ^= 1; }
+                if (++x == NVQ) { x = 0; ph ^= 1; }
             }
             if (el && mine) umma_commit(&bars[V_S + i]);
+            if (i == 1) { qs = x; qp = ph; }
         };
         if (ntu > 0) {
             wait(V_RES, 0);
-            scores(f == 0);
+            scores(0, f0 == 0);
+            scores(1, f1 == 0);
         }
         for (int j = 0; j < ntu; ++j) {
-            const int s0 = s;
-            wait(V_F + s, ph);
-            if (++s == NV) { s = 0; ph ^= 1; }
-            const int s1 = s;
-            wait(V_F + s, ph);
-            if (++s == NV) { s = 0; ph ^= 1; }
-            if (j >= f) {
-                const uint32_t v0 = r_lo + s0 * (UNIT / 16), v1 = r_lo + s1 * (UNIT / 16);
+            const int b = j & 1;
+            const bool more = j + 1 < ntu;
+            wait(V_DF + b, (j >> 1) & 1);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    wait((half ? V_PB : V_PA) + i, (j - f) & 1);
-                    tc_fence_after();
-                    if (el) {
+            for (int i = 0; i < 2; ++i) {
+                const int f = i ? f1 : f0;
+                if (j >= f) {
+                    const uint32_t d = tmem + TV_O + i * 128, p = tmem + TV_S + i * 128, v = d_lo + b * (2 * UNIT / 16);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t acc = (half > 0 || e > 0 || j > f) ? 1 : 0, step = (half * 4 + e) * 128;
-                            umma_ts(d_o, d_s + (half * 4 + e) * 8, desc64(v0 + step, hi), id_o, acc);
-                            umma_ts(d_o + 64, d_s + (half * 4 + e) * 8, desc64(v1 + step, hi), id_o, acc);
+                    for (int half = 0; half < 2; ++half) {
+                        wait((half ? V_PB : V_PA) + i, (j - f) & 1);
+                        tc_fence_after();
+                        if (el) {
+#pragma unroll
+                            for (int e = half * 4; e < half * 4 + 4; ++e)
+                                umma_ts(d, p + e * 8, desc64(v + e * 128, hi), id_o, (e > 0 || j > f) ? 1 : 0);
                         }
                     }
+                    if (el) umma_commit(&bars[V_PV + i]);
                 }
-                if (el) umma_commit(&bars[V_PV + i]);
+                if (i == 1 && el) umma_commit(&bars[V_DE + b]);
+                if (more) scores(i, j + 1 >= f);
             }
-            if (el) { umma_commit(&bars[V_E + s0]); umma_commit(&bars[V_E + s1]); }
-            if (j + 1 < ntu) scores(j + 1 >= f);
             if (*abort_flag) break;
         }
         if (el) {
-            umma_commit(&bars[V_DRAIN + i]);
-            if (!mbar_wait(&bars[V_DRAIN + i], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
+            umma_commit(&bars[V_DRAIN]);
+            if (!mbar_wait(&bars[V_DRAIN], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
         }
-    } else {
+    } else if (warp < W_LOAD) {
         // ============================================================================ P
         const int i = warp >> 2, quad = warp & 3;
         const uint32_t lanes = (uint32_t)quad << 21;
@@ -534,7 +541,7 @@ latent_dv_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_co
         float next = 0.f;
         auto fetch = [&](int tile) {
             const long long c = (long long)tile * TL + (tid & 127);
-            next = c < Lq ? st_lse[sp.q0 + c] : INFINITY;
+            next = c < Lq ? -st_lse[sp.q0 + c] : -INFINITY;
         };
         if (f < t_hi) fetch(f);
         for (int tile = f; tile < t_hi; ++tile) {
@@ -551,40 +558,38 @@ latent_dv_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_co
             // gradients of rows behind the sequence's last query may be anything: zeros, before the product reads them
             // (behind the wait for the scores: the ring slots' earlier uses are over by then, so the parity is this use's)
             if (c0 + TL > Lq) {
-                const int valid = (int)(Lq - c0), per = u1 + 2;
+                const int valid = (int)(Lq - c0), x = tile - t_lo;
+                wait(V_DF + (x & 1), (x >> 1) & 1);
                 for (int u = 0; u < 2; ++u) {
-                    const int x = (tile - t_lo) * per + u1 + u;
-                    wait(V_F + x % NV, (x / NV) & 1);
-                    unsigned char *un = sm + V_RING + (x % NV) * UNIT;
+                    unsigned char *un = sm + V_D + ((x & 1) * 2 + u) * UNIT;
                     for (int e = quad * 32 + lane; e < (TL - valid) * 8; e += 128)
                         *reinterpret_cast<uint4 *>(un + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
             }
-            float s[128];
-            tmem_ld64_sync(ts, *reinterpret_cast<float (*)[64]>(s));
-            tmem_ld64_sync(ts + 64, *reinterpret_cast<float (*)[64]>(s + 64));
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+                float s[64];
+                tmem_ld64_sync(ts + half * 64, s);
                 if (edge) {
 #pragma unroll
-                    for (int e = half * 64; e < half * 64 + 64; ++e) {
-                        const long long c = c0 + e;
+                    for (int e = 0; e < 64; ++e) {
+                        const long long c = c0 + half * 64 + e;
                         if (c < lo || c >= Lq) s[e] = -INFINITY;
                     }
                 }
+                uint32_t w[32];
+                const uint64_t sc2 = f2(sc, sc);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const int x = half * 64 + c * 32 + 2 * e;
-                        const float4 l4 = *reinterpret_cast<const float4 *>(stat + x);
-                        w[e] = pack_bf16x2(ex2(s[x] * sc - l4.x), ex2(s[x + 1] * sc - l4.y));
-                        w[e + 1] = pack_bf16x2(ex2(s[x + 2] * sc - l4.z), ex2(s[x + 3] * sc - l4.w));
-                    }
-                    tmem_st16u(ts + half * 32 + c * 16, w);
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 l4 = *reinterpret_cast<const float4 *>(stat + half * 64 + 2 * e);       // minus lse
+                    float x0, x1, x2, x3;
+                    f2_split(f2_fma(f2(s[2 * e], s[2 * e + 1]), sc2, f2(l4.x, l4.y)), x0, x1);
+                    f2_split(f2_fma(f2(s[2 * e + 2], s[2 * e + 3]), sc2, f2(l4.z, l4.w)), x2, x3);
+                    w[e] = pack_bf16x2(ex2(x0), ex2(x1));
+                    w[e + 1] = pack_bf16x2(ex2(x2), ex2(x3));
                 }
+                tmem_st32(ts + half * 32, w);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -617,6 +622,25 @@ latent_dv_kernel(LatentArgs a, LatentBwdArgs b, long long slots, const __grid_co
     if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
+// One launch for the three: blocks of dq, then of dk, then of dv, each kind from its longest row of tiles to its
+// shortest, so that a kind's last blocks do not leave the GPU idle.
+__global__ void __launch_bounds__(NT, 1)
+latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_slots, const __grid_constant__ GradMaps mq,
+                  const __grid_constant__ GradMaps mk)
+{
+    extern __shared__ __align__(1024) unsigned char sm[];
+    if (blockIdx.x == 0) {
+        check_offsets(a.cu_q, a.N, a.T, a.status);
+        check_offsets(a.cu_k, a.N, a.Tk, a.status);
+    }
+    if (smem_u32(sm) & 1023u) { if (threadIdx.x == 0) set_status(a.status, KDA_ERR_CUDA); return; }   // swizzled tiles need it (it holds)
+    const int h = blockIdx.x % a.H;
+    const long long x = blockIdx.x / a.H;
+    if (x < q_slots) grad_block<true>(a, b, q_slots - 1 - x, h, mq, sm);
+    else if (x < q_slots + k_slots) grad_block<false>(a, b, x - q_slots, h, mk, sm);
+    else dv_block(a, b, x - q_slots - k_slots, h, mk, sm);
+}
+
 // dr[key] = sum over heads of dr_head[key][h], in fp32 and in head order. 16 keys per block: 16 threads of a
 // float4 each per key.
 __global__ void __launch_bounds__(256) latent_dr_kernel(const float *__restrict__ dr_head, __nv_bfloat16 *__restrict__ dr, long long keys, int H)
@@ -641,9 +665,11 @@ bool al(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
 
 cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaStream_t stream)
 {
-    const long long tokens = (long long)a.B * a.T, keys = (long long)a.B * a.Tk, rows = tokens * a.H;
-    const long long q_slots = tokens / TL + a.N, k_slots = keys / TL + a.N, v_slots = keys / (2 * TL) + a.N;
-    if (q_slots * a.H > 0x7fffffffLL || k_slots * a.H > 0x7fffffffLL || rows / 8 >= 0x7fffffffLL) return cudaErrorInvalidValue;
+    const long long tokens = (long long)a.B * a.T, keys = (long long)a.B * a.Tk;
+    const long long q_slots = tokens > 0 ? tokens / TL + a.N : 0, k_slots = keys > 0 ? keys / TL + a.N : 0;
+    const long long v_slots = keys > 0 ? keys / (2 * TL) + a.N : 0;
+    if (q_slots + k_slots == 0) return cudaSuccess;
+    if ((q_slots + k_slots + v_slots) * a.H > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int W = kHeadDim + a.R;
     CUtensorMap q = {}, k = {}, r = {}, v = {}, d = {};          // an empty side's tiles are never copied
     if (tokens > 0 && (!bf16_heads_map(&q, a.q, W, a.H, tokens, W, (long long)a.H * W, 64, TL) ||
@@ -653,21 +679,14 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
                      !bf16_heads_map(&v, a.v, kHeadDim, a.H, keys, a.v_head, a.v_tok, 64, TL) ||
                      (a.R && !bf16_rows_map(&r, a.r, kSharedDim, keys, a.r_tok, 64, TL))))
         return cudaErrorNotSupported;
-    cudaError_t e;
-    if ((e = cudaFuncSetAttribute(latent_grad_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_END)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(latent_grad_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G_END)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(latent_dv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)V_END)) != cudaSuccess)
-        return e;
+    constexpr uint32_t smem = G_END > V_END ? G_END : V_END;
+    const cudaError_t e = cudaFuncSetAttribute(latent_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     const GradMaps mq = {q, q, d, k, r, v}, mk = {k, r, v, q, q, d};
-    if (tokens > 0) {
-        latent_stat_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(a.out, b.dout, a.lse, b.stat, tokens, a.H);
-        latent_grad_kernel<true><<<(unsigned)(q_slots * a.H), NT, G_END, stream>>>(a, b, q_slots, mq);
-    }
-    if (keys > 0) {
-        latent_grad_kernel<false><<<(unsigned)(k_slots * a.H), NT, G_END, stream>>>(a, b, k_slots, mk);
-        latent_dv_kernel<<<(unsigned)(v_slots * a.H), NT, V_END, stream>>>(a, b, v_slots, mk);
-        if (a.R) latent_dr_kernel<<<(unsigned)((keys + 15) / 16), 256, 0, stream>>>(b.dr_head, b.dr, keys, a.H);
-    }
+    if (tokens > 0)
+        latent_stat_kernel<<<(unsigned)(((tokens + 31) / 32 * a.H + 7) / 8), 256, 0, stream>>>(a.out, b.dout, a.lse, b.stat, tokens, a.H);
+    latent_bwd_kernel<<<(unsigned)((q_slots + k_slots + v_slots) * a.H), NT, smem, stream>>>(a, b, q_slots, k_slots, mq, mk);
+    if (a.R && keys > 0) latent_dr_kernel<<<(unsigned)((keys + 15) / 16), 256, 0, stream>>>(b.dr_head, b.dr, keys, a.H);
     return cudaGetLastError();
 }
 

@@ -31,10 +31,11 @@ using namespace sm100;
 constexpr int QT = 128, KT = 128;             // query rows of a tile (two per block), keys of a tile
 constexpr int NT = 8 * 32 + 64, W_LOAD = 8, W_MMA = 9;
 constexpr uint32_t UNIT = 16384;              // 128 rows x 64 channels, 128-byte swizzle
-constexpr uint32_t OFF_Q = 0, OFF_K = 6 * UNIT, OFF_V = OFF_K + 6 * UNIT, OFF_BAR = OFF_V + 2 * UNIT;   // two tiles of Q, two of K, one of V
+constexpr int NK = 4;                         // ring of key units
+constexpr uint32_t OFF_Q = 0, OFF_K = 6 * UNIT, OFF_V = OFF_K + NK * UNIT, OFF_BAR = OFF_V + 4 * UNIT;   // two tiles of Q, the keys' ring, two tiles of V
 constexpr uint32_t SMEM = OFF_BAR + 512 + 1024;
 static_assert(SMEM <= 232448, "shared memory");
-enum { B_Q, B_KF, B_KE = B_KF + 2, B_VF = B_KE + 2, B_VE, B_S, B_P = B_S + 2, B_PV = B_P + 2,
+enum { B_Q, B_KF, B_KE = B_KF + NK, B_VF = B_KE + NK, B_VE = B_VF + 2, B_S = B_VE + 2, B_PA = B_S + 2, B_PB = B_PA + 2, B_PV = B_PB + 2,
        B_DRAIN = B_PV + 2, N_BARS };
 constexpr uint32_t TM_S = 0, TM_O = 256;      // S (and P over it) of the two tiles, O of the two tiles
 
@@ -74,13 +75,13 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
     if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
     if (tid == 0) {
         mbar_init(&bars[B_Q], 1);
-        mbar_init(&bars[B_VF], 1);
-        mbar_init(&bars[B_VE], 1);
+        for (int i = 0; i < NK; ++i) { mbar_init(&bars[B_KF + i], 1); mbar_init(&bars[B_KE + i], 1); }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[B_KF + i], 1);
-            mbar_init(&bars[B_KE + i], 1);
+            mbar_init(&bars[B_VF + i], 1);
+            mbar_init(&bars[B_VE + i], 1);
             mbar_init(&bars[B_S + i], 1);
-            mbar_init(&bars[B_P + i], 4);
+            mbar_init(&bars[B_PA + i], 4);
+            mbar_init(&bars[B_PB + i], 4);
             mbar_init(&bars[B_PV + i], 1);
         }
         mbar_init(&bars[B_DRAIN], 1);
@@ -112,24 +113,29 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
                 for (int u = 0; u < kunits; ++u)
                     tma_load_3d(sm + OFF_Q + (i * 3 + u) * UNIT, &tm_q, &bars[B_Q], u * 64, (int)(t.q0 + i * QT), h);
             bool ok = true;
-            int j = 0;
+            int j = 0, s = 0, used = 0;
+            uint32_t ph = 0;
             for (; j < ntile; ++j) {
                 const int row = (int)(t.k0 + (long long)j * KT), b = j & 1;
-                unsigned char *kd = sm + OFF_K + b * 3 * UNIT;
-                if (j >= 2 && !(ok = wait(B_KE + b, ((j >> 1) - 1) & 1))) break;
-                mbar_arrive_expect_tx(&bars[B_KF + b], kunits * UNIT);
-                tma_load_3d(kd, &tm_k, &bars[B_KF + b], 0, row, h);
-                tma_load_3d(kd + UNIT, &tm_k, &bars[B_KF + b], 64, row, h);
-                if (a.R) tma_load_2d(kd + 2 * UNIT, &tm_r, &bars[B_KF + b], 0, row);
-                if (j >= 1 && !(ok = wait(B_VE, (j - 1) & 1))) break;
-                mbar_arrive_expect_tx(&bars[B_VF], 2 * UNIT);
-                tma_load_3d(sm + OFF_V, &tm_v, &bars[B_VF], 0, row, h);
-                tma_load_3d(sm + OFF_V + UNIT, &tm_v, &bars[B_VF], 64, row, h);
+                for (int u = 0; u < kunits; ++u) {
+                    if (used >= NK && !(ok = wait(B_KE + s, ph ^ 1))) break;
+                    unsigned char *kd = sm + OFF_K + s * UNIT;
+                    mbar_arrive_expect_tx(&bars[B_KF + s], UNIT);
+                    if (u < 2) tma_load_3d(kd, &tm_k, &bars[B_KF + s], u * 64, row, h);
+                    else tma_load_2d(kd, &tm_r, &bars[B_KF + s], 0, row);
+                    ++used;
+                    if (++s == NK) { s = 0; ph ^= 1; }
+                }
+                if (!ok || (j >= 2 && !(ok = wait(B_VE + b, ((j >> 1) - 1) & 1)))) break;
+                unsigned char *vd = sm + OFF_V + b * 2 * UNIT;
+                mbar_arrive_expect_tx(&bars[B_VF + b], 2 * UNIT);
+                tma_load_3d(vd, &tm_v, &bars[B_VF + b], 0, row, h);
+                tma_load_3d(vd + UNIT, &tm_v, &bars[B_VF + b], 64, row, h);
             }
             if (!ok) {                          // a wait ran out: what is in flight lands before the block ends
                 mbar_wait(&bars[B_Q], 0, 100000000LL);
-                for (int x = max(0, j - 1); x <= j && x < ntile; ++x) mbar_wait(&bars[B_KF + (x & 1)], (x >> 1) & 1, 100000000LL);
-                if (j > 0) mbar_wait(&bars[B_VF], (j - 1) & 1, 100000000LL);
+                for (int x = max(0, used - NK); x < used; ++x) mbar_wait(&bars[B_KF + x % NK], (x / NK) & 1, 100000000LL);
+                for (int x = max(0, j - 2); x < j; ++x) mbar_wait(&bars[B_VF + (x & 1)], (x >> 1) & 1, 100000000LL);
             }
         }
     } else if (warp == W_MMA) {
@@ -141,53 +147,57 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
         const uint32_t q_lo = desc_lo(sbase + OFF_Q, 16), k_lo = desc_lo(sbase + OFF_K, 16), v_lo = desc_lo(sbase + OFF_V, UNIT);
         const int nt0 = __reduce_max_sync(0xffffffffu, nt[0]), nt1 = __reduce_max_sync(0xffffffffu, nt[1]);
         const int ntu = max(nt0, nt1);
-        const bool has_r = a.R != 0;
-        auto scores = [&](int i, int b) {
-            if (el) {
-                const uint32_t q = q_lo + i * (3 * UNIT / 16), k = k_lo + b * (3 * UNIT / 16), d = tmem + TM_S + i * 128;
+        int ks = 0;                             // ring slot of the next key unit, its phase
+        uint32_t kp = 0;
+        // S of tile 0 (which waits for the units as they land), and of tile 1 (which frees them) if it has this one
+        auto scores = [&](int i, bool mine) {
+            int x = ks;
+            uint32_t ph = kp;
+            for (int u = 0; u < kunits; ++u) {
+                if (i == 0) { wait(B_KF + x, ph); tc_fence_after(); }
+                if (el) {
+                    if (mine) {
+                        const uint32_t q = q_lo + (i * 3 + u) * (UNIT / 16), k = k_lo + x * (UNIT / 16), d = tmem + TM_S + i * 128;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    umma_ss(d, desc64(q + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), desc64(k + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), id_s, e > 0 ? 1 : 0);
-                if (has_r) {
-#pragma unroll
-                    for (int e = 8; e < 12; ++e)
-                        umma_ss(d, desc64(q + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), desc64(k + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), id_s, 1);
+                        for (int e = 0; e < 4; ++e) umma_ss(d, desc64(q + e * 2, hi), desc64(k + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
+                    }
+                    if (i == 1) umma_commit(&bars[B_KE + x]);
                 }
-                umma_commit(&bars[B_S + i]);
+                if (++x == NK) { x = 0; ph ^= 1; }
             }
+            if (el && mine) umma_commit(&bars[B_S + i]);
+            if (i == 1) { ks = x; kp = ph; }
         };
         if (ntu > 0) {
             wait(B_Q, 0);
-            wait(B_KF, 0);
-            tc_fence_after();
-            if (nt0 > 0) scores(0, 0);
-            if (nt1 > 0) scores(1, 0);
-            if (el) umma_commit(&bars[B_KE]);
+            scores(0, nt0 > 0);
+            scores(1, nt1 > 0);
         }
         for (int j = 0; j < ntu; ++j) {
-            const int b = (j + 1) & 1;
+            const int b = j & 1;
             const bool more = j + 1 < ntu;
-            wait(B_VF, j & 1);
+            wait(B_VF + b, (j >> 1) & 1);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int nti = i ? nt1 : nt0;
                 if (j < nti) {
-                    // O_i += P_i V
-                    const uint32_t d = tmem + TM_O + i * 128, p = tmem + TM_S + i * 128;
-                    wait(B_P + i, j & 1);
-                    tc_fence_after();
-                    if (el) {
+                    // O_i += P_i V, the first 64 keys and then the others
+                    const uint32_t d = tmem + TM_O + i * 128, p = tmem + TM_S + i * 128, v = v_lo + b * (2 * UNIT / 16);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            umma_ts(d, p + e * 8, desc64(v_lo + e * 128, hi), id_o, (e > 0 || j > 0) ? 1 : 0);
-                        umma_commit(&bars[B_PV + i]);
+                    for (int half = 0; half < 2; ++half) {
+                        wait((half ? B_PB : B_PA) + i, j & 1);
+                        tc_fence_after();
+                        if (el) {
+#pragma unroll
+                            for (int e = half * 4; e < half * 4 + 4; ++e)
+                                umma_ts(d, p + e * 8, desc64(v + e * 128, hi), id_o, (e > 0 || j > 0) ? 1 : 0);
+                        }
                     }
+                    if (el) umma_commit(&bars[B_PV + i]);
                 }
-                if (i == 1 && el) umma_commit(&bars[B_VE]);
-                if (i == 0 && more) { wait(B_KF + b, ((j + 1) >> 1) & 1); tc_fence_after(); }
-                if (j + 1 < nti) scores(i, b);
+                if (i == 1 && el) umma_commit(&bars[B_VE + b]);
+                if (more) scores(i, j + 1 < nti);
             }
-            if (more && el) umma_commit(&bars[B_KE + b]);
             if (*abort_flag) break;
         }
         if (el) {
@@ -213,46 +223,55 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
             tc_fence_after();
             const int kb = j * KT;
             const bool edge = kb + KT > lim_warp;
-            // P with the maximum of the tiles before; l gets its sums in pairs
+            // P of 64 columns with the maximum so far, and its sum (taken in pairs). All exponentials go to the
+            // special-function unit: a polynomial on the FMA units for a quarter of them cost more in issue slots,
+            // which the issuing warps lack, than it saved (8K x 32 heads: 576 us for 537).
             const uint64_t sc2 = f2(sc, sc);
-            uint32_t w[64];
-            float sum;
-            auto exps = [&]() {
+            uint32_t w[32];
+            auto load = [&](int c, float (&s)[64]) {
+                tmem_ld64_sync(ts + c, s);
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) s[e] = kb + c + e < lim ? s[e] : -INFINITY;
+                }
+            };
+            auto exps = [&](const float (&s)[64]) {
                 const uint64_t m2 = f2(-m, -m);
                 uint64_t sum2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float s[64];
-                    tmem_ld64_sync(ts + c * 64, s);
-                    if (edge) {
-#pragma unroll
-                        for (int e = 0; e < 64; ++e) s[e] = kb + c * 64 + e < lim ? s[e] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float x0, x1;
-                        f2_split(f2_fma(f2(s[2 * e], s[2 * e + 1]), sc2, m2), x0, x1);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        sum2[e & 1] = f2_add(sum2[e & 1], f2(p0, p1));
-                        w[c * 32 + e] = pack_bf16x2(p0, p1);
-                    }
+                for (int e = 0; e < 32; ++e) {
+                    float x0, x1;
+                    f2_split(f2_fma(f2(s[2 * e], s[2 * e + 1]), sc2, m2), x0, x1);
+                    const float p0 = ex2(x0), p1 = ex2(x1);
+                    sum2[e & 1] = f2_add(sum2[e & 1], f2(p0, p1));
+                    w[e] = pack_bf16x2(p0, p1);
                 }
                 float s0, s1;
                 f2_split(f2_add(sum2[0], sum2[1]), s0, s1);
                 return s0 + s1;
             };
-            sum = exps();
-            // A sum that large (or none: no maximum yet, or a score that is not finite) means that some score is far
-            // above the maximum. Few tiles come here: the row's maximum, O and l scaled to it, and P again.
-            if (__any_sync(0xffffffffu, !(sum < 32768.f))) {
-                float top = -INFINITY;
-#pragma unroll 1
-                for (int c = 0; c < 128; c += 16) {
-                    float s[16];
-                    tmem_ld16_sync(ts + c, s);
+            auto publish = [&](int half) {                // over S's columns that are read already
+                tmem_st32(ts + half * 32, w);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[(half ? B_PB : B_PA) + i]);
+            };
+            float s[64];
+            load(0, s);
+            float sum = exps(s);
+            load(64, s);
+            float t0 = max3(s[0], s[1], s[2]), t1 = max3(s[3], s[4], s[5]);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) top = fmaxf(top, kb + c + e < lim ? s[e] : -INFINITY);
-                }
+            for (int e = 6; e < 62; e += 4) { t0 = max3(t0, s[e], s[e + 1]); t1 = max3(t1, s[e + 2], s[e + 3]); }
+            const float top_b = max3(t0, t1, fmaxf(s[62], s[63]));
+            // A sum or a score that large (or not finite, or no maximum yet) means that the maximum has to move. Few
+            // tiles come here: the row's maximum, O and l scaled to it, and the first half again.
+            if (__any_sync(0xffffffffu, !(sum < 32768.f) || top_b * sc > m + 15.f)) {
+                load(0, s);
+                float top = top_b;
+#pragma unroll
+                for (int e = 0; e < 64; ++e) top = fmaxf(top, s[e]);
                 const float up = fmaxf(m, top * sc), f = up == m ? 1.f : ex2(m - up);
                 m = up;
                 l *= f;
@@ -270,24 +289,22 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
                     }
                     tmem_st_wait();
                 }
-                sum = exps();
+                sum = exps(s);
+                load(64, s);
             }
-            l += sum;
             // values behind the sequence's last key may be anything: zeros, before the second product reads them
             if (kb + KT > t.kn) {
                 const int valid = (int)(t.kn - kb);
-                wait(B_VF, j & 1);
+                wait(B_VF + (j & 1), (j >> 1) & 1);
                 for (int u = 0; u < 2; ++u)
                     for (int e = quad * 32 + lane; e < (KT - valid) * 8; e += 128)
-                        *reinterpret_cast<uint4 *>(sm + OFF_V + u * UNIT + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(sm + OFF_V + ((j & 1) * 2 + u) * UNIT + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
                 fence_proxy_async_smem();
             }
-            tmem_st32(ts, *reinterpret_cast<uint32_t (*)[32]>(w));          // over S, which is read
-            tmem_st32(ts + 32, *reinterpret_cast<uint32_t (*)[32]>(w + 32));
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[B_P + i]);
+            publish(0);
+            sum += exps(s);
+            publish(1);
+            l += sum;
         }
         if (nti > 0) {
             wait(B_PV + i, (nti - 1) & 1);

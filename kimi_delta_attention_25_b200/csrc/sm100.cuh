@@ -430,25 +430,6 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-// 2^x of a pair on the FMA units, for finite x below 2^7 (below -126 the result is that of -126): x = n + f with
-// |f| <= 1/2 by adding and taking away 1.5 2^23, whose sum has n in its low bits; 2^f by the polynomial of
-// degree 4 with the least relative error on [-1/2, 1/2] (2.7e-6, a Lawson fit; less than a thousandth of what
-// rounding the result to bf16 does), and n added to the exponent.
-__device__ __forceinline__ void ex2_poly(float x0, float x1, float &p0, float &p1) {
-    const uint64_t x = f2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-    const uint64_t r = f2_add(x, f2(12582912.f, 12582912.f));
-    const uint64_t f = f2_fma(f2_add(r, f2(-12582912.f, -12582912.f)), f2(-1.f, -1.f), x);
-    uint64_t p = f2_fma(f2(0.009570102f, 0.009570102f), f, f2(0.05591786f, 0.05591786f));
-    p = f2_fma(p, f, f2(0.24024744f, 0.24024744f));
-    p = f2_fma(p, f, f2(0.6931218f, 0.6931218f));
-    p = f2_fma(p, f, f2(0.9999993f, 0.9999993f));
-    float r0, r1;
-    f2_split(r, r0, r1);
-    f2_split(p, p0, p1);
-    p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(r0) << 23));
-    p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(r1) << 23));
-}
-
 // Largest of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
