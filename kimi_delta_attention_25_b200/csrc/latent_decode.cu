@@ -91,6 +91,23 @@ __device__ __forceinline__ bool bar_or(uint32_t id, uint32_t nthreads, bool mine
     return r != 0;
 }
 
+// 16 values of each of lanes 0..15 (and of 16..31 among themselves), combined over the lanes: lane i (i + 16) gets
+// the result of value i. Each exchange halves the values a lane still has.
+template <typename Op>
+__device__ __forceinline__ float spread16(float (&v)[16], int lane, Op op)
+{
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) {
+        const bool upper = lane & w;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float send = upper ? v[i] : v[i + w], keep = upper ? v[i + w] : v[i];
+            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, w));
+        }
+    }
+    return v[0];
+}
+
 __device__ __forceinline__ int tiles_of(const DecodeArgs &a, int n, int *len_out, bool *bad)
 {
     const int len = a.lens[n];
@@ -111,8 +128,8 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int share = blockIdx.x / a.G, g = blockIdx.x % a.G;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Y::BAR);
-    volatile int *ctl = reinterpret_cast<volatile int *>(bars + N_BARS);   // [0] tmem, [1] abort, [2] error, [3] n0, [4] off0
-    __shared__ long long s_warp[NT / 32], s_prefix;
+    volatile int *ctl = reinterpret_cast<volatile int *>(bars + N_BARS);   // [0] tmem, [1] abort, [2] error, [3] n0, [4] off0, [5] prefix
+    __shared__ int s_warp[NT / 32];
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
@@ -129,7 +146,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         }
         for (int i = 0; i < Y::NSLOT; ++i) { mbar_init(&bars[B_FULL + i], 1); mbar_init(&bars[B_EMPTY + i], 1); }
         mbar_init(&bars[B_DRAIN], 1);
-        ctl[1] = 0; ctl[2] = 0; ctl[3] = a.N; ctl[4] = 0; s_prefix = 0;
+        ctl[1] = 0; ctl[2] = 0; ctl[3] = a.N; ctl[4] = 0; ctl[5] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_c);
@@ -137,46 +154,39 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
     // The list of tiles: each thread counts a run of sequences, then finds whether this share begins in it.
     const int per = (a.N + NT - 1) / NT, n_lo = min(a.N, tid * per), n_hi = min(a.N, n_lo + per);
     bool bad = false;
-    long long mine = 0;
+    int mine = 0;                                              // (the host sees to it that the list fits 31 bits)
     for (int n = n_lo; n < n_hi; ++n) { int len; mine += tiles_of(a, n, &len, &bad); }
-    long long upto = mine;                                     // inclusive sums: within the warp, then over the warps
+    int upto = mine;                                           // inclusive sums: within the warp, then over the warps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += v;
     }
     if (lane == 31) s_warp[warp] = upto;
     __syncthreads();
-    long long total = 0;
+    int total = 0;
 #pragma unroll
     for (int w = 0; w < NT / 32; ++w) {
         if (w < warp) upto += s_warp[w];
         total += s_warp[w];
     }
-    // shares that get tiles: with fewer tiles than shares one each, so that no share inside a cut sequence is empty
-    const int used = (int)min((long long)a.L, total);
-    const long long begin = share < used ? total * share / used : 0, end = share < used ? total * (share + 1) / used : 0;
+    // shares that get tiles: with fewer tiles than shares one each, so that no share inside a cut sequence is empty;
+    // the first `longer` shares have base + 1 tiles, the others base
+    const uint32_t used = min(a.L, total), base = used ? (uint32_t)total / used : 0, longer = used ? (uint32_t)total % used : 0;
+    const int ntiles = share < (int)used ? (int)(base + (share < (int)longer ? 1 : 0)) : 0;
+    const int begin = (int)(share * base + min((uint32_t)share, longer));
     {
-        long long at = upto - mine;
-        if (begin >= at && begin < at + mine && begin < end)
+        int at = upto - mine;
+        if (ntiles > 0 && begin >= at && begin < upto)
             for (int n = n_lo; n < n_hi; ++n) {
                 int len;
                 const int t = tiles_of(a, n, &len, &bad);
-                if (begin < at + t) { ctl[3] = n; ctl[4] = (int)(begin - at); s_prefix = at; break; }
+                if (begin < at + t) { ctl[3] = n; ctl[4] = begin - at; ctl[5] = at; break; }
                 at += t;
             }
     }
     if (bad) ctl[2] = KDA_ERR_INVALID_ARG;
     const int rows = min(RG, a.Tq * a.H - g * RG);             // this group's query rows
-    for (int n = share; n < a.N; n += a.L) {                   // idle slots: nothing to attend to
-        int len;
-        if (tiles_of(a, n, &len, &bad) == 0) {
-            const size_t r0 = (size_t)n * a.Tq * a.H + g * RG;
-            for (int i = tid; i < rows * (kLatentDim / 8); i += NT)
-                reinterpret_cast<uint4 *>(a.out + r0 * kLatentDim)[i] = make_uint4(0, 0, 0, 0);
-            for (int i = tid; i < rows; i += NT) a.lse[r0 + i] = -INFINITY;
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -200,14 +210,19 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         // ============================================================================ loader
         // The warp's lanes share a tile's copies: one per 64-channel half and box of rows.
         const int nb = KT / a.box, b = lane % nb;
-        int it = 0, seg = 0, n = n0, off = off0, slots_used = 0, slot_next = 0, slot_phase = 0;
-        long long left = end - begin;
+        int it = 0, seg = 0, n = n0, off = off0, slots_used = 0, slot_next = 0, slot_phase = 0, left = ntiles;
         bool ok = true;
         while (left > 0 && ok) {
             int len;
             bool x = false;
-            const int tiles = tiles_of(a, n, &len, &x), cnt = (int)min((long long)(tiles - off), left);
+            const int tiles = tiles_of(a, n, &len, &x), cnt = min(tiles - off, left);
             if (cnt <= 0) { ++n; off = 0; continue; }
+            auto load_q = [&]() {
+                if (lane == 0) mbar_arrive_expect_tx(&bars[B_QFULL], chunks * Y::QCHUNK);
+                __syncwarp();
+                if (lane < chunks) tma_load_2d(sm + Y::Q + lane * Y::QCHUNK, &tm_q, &bars[B_QFULL], lane * 64, n * a.Tq * a.H + g * RG);
+            };
+            if (seg == 0) load_q();
             // row coordinate of this lane's box in tile t; behind the last row, or on a page that is not there, the
             // copy starts behind the cache and reads zeros
             // (the table's entry is read a tile ahead and looked at when its turn comes)
@@ -243,19 +258,26 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                     if (half < 2) tma_load_2d(sm + Y::RING + s * SLOT + half * 8192 + b * a.box * 128, &tm_c, &bars[B_FULL + s], c * 128 + half * 64, c1);
                     slots_used = i + 1;
                     if (++slot_next == Y::NSLOT) { slot_next = 0; slot_phase ^= 1; }
-                    if (c == 1 && t == off) {
+                    if (c == 1 && t == off && seg > 0) {
                         // the sequence's queries, once the last segment's scores are done (not in front of the cache
                         // rows, which need not wait; not behind them all, as the ring may be too short for that)
-                        if (seg > 0) ok = wait(B_QEMPTY, (seg - 1) & 1);
-                        ok = __all_sync(0xffffffffu, ok);
+                        ok = __all_sync(0xffffffffu, wait(B_QEMPTY, (seg - 1) & 1));
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(&bars[B_QFULL], chunks * Y::QCHUNK);
-                        __syncwarp();
-                        if (lane < chunks) tma_load_2d(sm + Y::Q + lane * Y::QCHUNK, &tm_q, &bars[B_QFULL], lane * 64, n * a.Tq * a.H + g * RG);
+                        load_q();
                     }
                 }
             }
             ++seg; left -= cnt; ++n; off = 0;
+        }
+        for (int i = share; i < a.N; i += a.L) {               // idle slots: nothing to attend to
+            int len;
+            bool x = false;
+            if (tiles_of(a, i, &len, &x) == 0) {
+                const size_t r0 = (size_t)i * a.Tq * a.H + g * RG;
+                for (int e = lane; e < rows * (kLatentDim / 8); e += 32)
+                    reinterpret_cast<uint4 *>(a.out + r0 * kLatentDim)[e] = make_uint4(0, 0, 0, 0);
+                for (int e = lane; e < rows; e += 32) a.lse[r0 + e] = -INFINITY;
+            }
         }
         // copies still in flight (only after a wait ran out) land before the block ends
         if (!ok && lane == 0) {
@@ -277,7 +299,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         // whose RG values a row are one swizzle atom wide
         const uint32_t q_lo = desc_lo(sbase + Y::Q, 16), p_lo = desc_lo(sbase + Y::P, 16), sh_lo = desc_lo(sbase + Y::SH, 16);
         const uint32_t k_lo = desc_lo(sbase + Y::RING, 16), v_lo = desc_lo(sbase + Y::RING, 8192);
-        const int ntile = __reduce_max_sync(0xffffffffu, (int)(end - begin));
+        const int ntile = __reduce_max_sync(0xffffffffu, ntiles);
         const uint32_t has_r = a.R != 0;
         int n = n0, off = off0, seg = 0, seg_left = 0;
         int sslot = 0, pslot = 0;
@@ -365,16 +387,16 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         const int key = quad * 16 + lane;                    // lanes below 16
         float *red = reinterpret_cast<float *>(sm + Y::RED), *fac = reinterpret_cast<float *>(sm + Y::FAC);
         float *mseg = reinterpret_cast<float *>(sm + Y::MAXS);
-        long long j = 0;                                     // tile of this share
-        int n = n0, off = off0;
-        long long left = end - begin, pfx = s_prefix;        // pfx: tiles before sequence n
+        int j = 0;                                           // tile of this share
+        int n = n0, off = off0, left = ntiles, pfx = ctl[5]; // pfx: tiles before sequence n
         int cut_n = -1, cut_last = 0;
         while (left > 0) {
             int len;
             bool x = false;
-            const int tiles = tiles_of(a, n, &len, &x), cnt = (int)min((long long)(tiles - off), left);
+            const int tiles = tiles_of(a, n, &len, &x), cnt = min(tiles - off, left);
             if (cnt <= 0) { ++n; off = 0; continue; }
-            float m[HP], lsum[HP];                           // running maxima (log2 domain), this thread's part of the sums
+            // running maxima (log2 domain; lane i < 16 also has row i's in m_l), this thread's part of the sums
+            float m[HP], lsum[HP], m_l = lane < HP && grp * HP + lane < rows ? kNone : kOff;
 #pragma unroll
             for (int i = 0; i < HP; ++i) { m[i] = grp * HP + i < rows ? kNone : kOff; lsum[i] = 0.f; }
             for (int t = off; t < off + cnt; ++t, ++j) {
@@ -415,20 +437,24 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                     fence_proxy_async_smem();
                 }
                 if (bar_or(1, NSOFT, top > 8.f)) {           // the same outcome in all warps
+                    float v[HP];
 #pragma unroll
-                    for (int i = 0; i < HP; ++i) {
-                        const float mx = warp_max(s[i]);
-                        if (lane == 0) red[quad * RG + grp * HP + i] = mx;
-                    }
+                    for (int i = 0; i < HP; ++i) v[i] = s[i];
+                    const float mine16 = spread16(v, lane, [](float x, float y) { return fmaxf(x, y); });
+                    if (lane < HP) red[quad * RG + grp * HP + lane] = mine16;
                     named_bar_sync(1, NSOFT);
+                    float f_l = 1.f;
+                    if (lane < HP) {
+                        const float *r = red + grp * HP + lane;
+                        const float up = fmaxf(m_l, fmaxf(fmaxf(r[0], r[RG]), fmaxf(r[2 * RG], r[3 * RG])) * a.scale_log2);
+                        if (up != m_l) f_l = ex2(m_l - up);
+                        m_l = up;
+                        if (quad == 0) fac[grp * HP + lane] = f_l;
+                    }
 #pragma unroll
                     for (int i = 0; i < HP; ++i) {
-                        const int r = grp * HP + i;
-                        const float mx = fmaxf(fmaxf(red[r], red[RG + r]), fmaxf(red[2 * RG + r], red[3 * RG + r])) * a.scale_log2;
-                        const float up = fmaxf(m[i], mx), f = up == m[i] ? 1.f : ex2(m[i] - up);
-                        m[i] = up;
-                        lsum[i] *= f;
-                        if (quad == 0 && lane == 0) fac[r] = f;
+                        m[i] = __shfl_sync(0xffffffffu, m_l, i);
+                        lsum[i] *= __shfl_sync(0xffffffffu, f_l, i);
                     }
                     named_bar_sync(1, NSOFT);
                     if (t > off) {
@@ -475,18 +501,13 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
                 if (lane == 0) mbar_arrive(&bars[B_PREADY + buf]);
             }
             // -------- the segment's results
-#pragma unroll
-            for (int i = 0; i < HP; ++i) {
-                float v = lane < 16 ? lsum[i] : 0.f;
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                if (lane == 0) {
-                    red[quad * RG + grp * HP + i] = v;
-                    if (quad == 0) mseg[grp * HP + i] = m[i];
-                }
+            // (lanes above 15 have added zeros)
+            const float mine16 = spread16(lsum, lane, [](float x, float y) { return x + y; });
+            if (lane < HP) {
+                red[quad * RG + grp * HP + lane] = mine16;
+                if (quad == 0) mseg[grp * HP + lane] = m_l;
             }
-            const long long jl = j - 1;
-            wait(B_PVDONE + (jl & 1), (uint32_t)(jl >> 1) & 1);
+            wait(B_PVDONE + ((j - 1) & 1), (uint32_t)((j - 1) >> 1) & 1);
             __syncwarp();
             tc_fence_after();
             named_bar_sync(1, NSOFT);
@@ -506,24 +527,27 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
             for (int c = grp; c < 4; c += Y::WG) {
                 const int dim = c * 128 + quad * 32 + lane;
 #pragma unroll 1
-                for (int q = 0; q < RG / 16; ++q) {
-                    if (q * 16 >= rows) break;
+                for (int q = 0; q * 16 < rows; ++q) {
                     float o[16];
                     tmem_ld16_sync(TM_O + lanes + c * RG + q * 16, o);
+                    const int upto = rows - q * 16;
+                    if (whole) {
+                        __nv_bfloat16 *dst = a.out + (r0 + q * 16) * kLatentDim + dim;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int r = q * 16 + i;
-                        if (r < rows) {
-                            if (whole) a.out[(r0 + r) * kLatentDim + dim] = __float2bfloat16_rn(o[i] * fac[r]);
-                            else a.part[(pslot * RG + r) * kLatentDim + dim] = o[i];
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            if (i < upto) dst[i * kLatentDim] = __float2bfloat16_rn(o[i] * fac[q * 16 + i]);
+                    } else {
+                        float *dst = a.part + (pslot * RG + q * 16) * kLatentDim + dim;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < upto) dst[i * kLatentDim] = o[i];
                     }
                 }
             }
             if (!whole && off == 0) {                        // cut at this share's end: who joins it
                 cut_n = n;
-                const long long last = pfx + tiles - 1;
-                cut_last = (int)(((last + 1) * used - 1) / total);
+                const uint32_t last = (uint32_t)(pfx + tiles - 1), head = longer * (base + 1);
+                cut_last = (int)(last < head ? last / (base + 1) : longer + (last - head) / base);
             }
             tc_fence_before();
             named_bar_sync(1, NSOFT);                        // the sums and O are read before the next segment
@@ -720,7 +744,7 @@ kda_status_t kda_latent_decode_step(const void *q, const void *cache, const int3
     if (!(scale > 0.f) || scale > 3.0e38f) return KDA_ERR_INVALID_ARG;
     if (dtype != KDA_BF16 || dc != kLatentDim || (dr != 0 && dr != kSharedDim) || page_size % 16 != 0) return KDA_ERR_UNSUPPORTED;
     if (num_pages * page_size > 0x7fff0000LL || (long long)max_pages * page_size > 0x7fff0000LL ||
-        (long long)Tq * H > 65536 || (long long)N * Tq * H > 0x7fff0000LL || N > kMaxGridDim)
+        (long long)N * ((long long)max_pages * page_size / KT + 1) > 0x7fffffffLL || (long long)Tq * H > 65536 || (long long)N * Tq * H > 0x7fff0000LL || N > kMaxGridDim)
         return KDA_ERR_UNSUPPORTED;
     if (!workspace || !al(workspace, 16) || workspace_bytes < kda_latent_decode_workspace_size(N, Tq, H)) return KDA_ERR_INVALID_ARG;
     cudaStream_t st = (cudaStream_t)stream;

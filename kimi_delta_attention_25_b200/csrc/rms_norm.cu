@@ -143,12 +143,12 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) rms_norm_kernel(NormPar
                 m = (m != m) ? m : (other != other ? other : fmaxf(m, other));
             }
             const float s = m / kE4m3Max;
-            const float inv = s == 0.f ? 0.f : 1.f / s;
+            const float d = s == 0.f ? 1.f : s;
             if (v < nvec) {
                 uint16_t q[NV / 2];
 #pragma unroll
                 for (int e = 0; e < NV; e += 2)
-                    q[e / 2] = __nv_cvt_float2_to_fp8x2(make_float2(y[e] * inv, y[e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                    q[e / 2] = __nv_cvt_float2_to_fp8x2(make_float2(y[e] / d, y[e + 1] / d), __NV_SATFINITE, __NV_E4M3);
                 if constexpr (NV == 8) {
                     reinterpret_cast<uint2 *>(p.y)[base + v] =
                         make_uint2(q[0] | ((uint32_t)q[1] << 16), q[2] | ((uint32_t)q[3] << 16));

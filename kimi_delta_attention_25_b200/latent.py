@@ -7,6 +7,8 @@ on one CUDA device; the work is enqueued on that device's current stream.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 import kimi_delta_attention_25_b200 as _kda
@@ -16,29 +18,43 @@ _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int6
 
 
 def _check(name, t, dtype, dev, shape=None, dense=True):
-    """One tensor argument: type, device, shape and (``dense``) contiguity."""
+    """One tensor argument: type, device (by index), shape and (``dense``) contiguity."""
+    if t.dtype is dtype and t.get_device() == dev >= 0 and (shape is None or t.shape == shape) and (
+            not dense or t.is_contiguous()):
+        return
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, str(dtype).replace("torch.", ""), t.dtype))
-    if not t.is_cuda:
+    if not t.is_cuda or dev < 0:
         raise ValueError("libkda takes CUDA tensors only (no CPU fallback)")
-    if t.device != dev:
-        raise ValueError("%s is on %s, the call's other tensors on %s" % (name, t.device, dev))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, the call's other tensors on cuda:%d" % (name, t.device, dev))
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if dense and not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s must be contiguous" % name)
+
+
+_FNS = {}
 
 
 def _call(name, dev, args):
-    """The C entry point on the tensors' device and its current stream; raises on a status."""
-    fn = getattr(_kda.load(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    """The C entry point on device ``dev`` and its current stream; raises on a status. (The tensors were
+    checked to be on that device; torch's context manager is entered only when it is not the current one.)"""
+    fn = _FNS.get(name)
+    if fn is None:
+        fn = _FNS[name] = getattr(_kda.load(), name)
+    if dev == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != _kda.KDA_OK:
         raise _kda.KDAError(st, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _size(name, *dims):
+    """A workspace size, which depends on the arguments alone."""
+    return int(getattr(_kda.load(), name)(*dims))
 
 
 def _p(t):
@@ -59,7 +75,7 @@ def _expanded(q, k, v, k_shared, cu_q, cu_k):
     """Checks of the expanded form's inputs; sizes and strides as the C call takes them."""
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k and v must be [B, T, H, D]")
-    dev = q.device
+    dev = q.get_device()
     B, T, H, W = q.shape
     Tk = k.shape[1]
     dr = 0 if k_shared is None else k_shared.shape[-1]
@@ -83,10 +99,10 @@ def _expanded(q, k, v, k_shared, cu_q, cu_k):
     return dev, (B, T, Tk, H, N, k.shape[-1], v.shape[-1], dr), (*ks, *vs, rs)
 
 
-def _workspace(workspace, size, dev):
+def _workspace(workspace, size, like):
     if workspace is None:
-        return torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
-    _check("workspace", workspace, torch.uint8, dev)
+        return torch.empty(max(size, 256), dtype=torch.uint8, device=like.device)
+    _check("workspace", workspace, torch.uint8, like.get_device())
     return workspace
 
 
@@ -103,14 +119,14 @@ def latent_fwd(q, k, v, k_shared=None, cu_seqlens=None, cu_seqlens_k=None, causa
     dev, dims, strides = _expanded(q, k, v, k_shared, cu_seqlens, cu_seqlens_k)
     B, T, Tk, H, N, _, dv, dr = dims
     if out is None:
-        out = torch.empty(B, T, H, dv, dtype=_BF16, device=dev)
+        out = q.new_empty((B, T, H, dv))
     else:
         _check("out", out, _BF16, dev, (B, T, H, dv))
     if lse is None:
-        lse = torch.empty(B, T, H, dtype=_F32, device=dev)
+        lse = q.new_empty((B, T, H), dtype=_F32)
     else:
         _check("lse", lse, _F32, dev, (B, T, H))
-    ws = _workspace(workspace, _kda.load().kda_latent_fwd_workspace_size(B, T, Tk, H, N, dr), dev)
+    ws = _workspace(workspace, _size("kda_latent_fwd_workspace_size", B, T, Tk, H, N, dr), q)
     _call("kda_latent_fwd", dev, (_p(q), _p(k), _p(v), _p(k_shared), _p(cu_seqlens), _p(cu_seqlens_k), _p(out), _p(lse),
                                   *dims, *strides, 1 if causal else 0, q.shape[-1] ** -0.5 if scale is None else scale,
                                   _kda.KDA_BF16, _p(ws), ws.numel()))
@@ -118,7 +134,7 @@ def latent_fwd(q, k, v, k_shared=None, cu_seqlens=None, cu_seqlens_k=None, causa
 
 
 def latent_bwd_workspace_size(B, T, Tk, H, N, dr=64) -> int:
-    return int(_kda.load().kda_latent_bwd_workspace_size(B, T, Tk, H, N, dr))
+    return _size("kda_latent_bwd_workspace_size", B, T, Tk, H, N, dr)
 
 
 def latent_bwd(q, k, v, k_shared, out, lse, dout, cu_seqlens=None, cu_seqlens_k=None, causal=True, scale=None, grads=None,
@@ -139,10 +155,10 @@ def latent_bwd(q, k, v, k_shared, out, lse, dout, cu_seqlens=None, cu_seqlens_k=
         if shape is None:
             g[key] = None
         elif g.get(key) is None:
-            g[key] = torch.empty(shape, dtype=_BF16, device=dev)
+            g[key] = q.new_empty(shape)
         else:
             _check(key, g[key], _BF16, dev, shape)
-    ws = _workspace(workspace, latent_bwd_workspace_size(B, T, Tk, H, N, dr), dev)
+    ws = _workspace(workspace, latent_bwd_workspace_size(B, T, Tk, H, N, dr), q)
     _call("kda_latent_bwd", dev, (_p(q), _p(k), _p(v), _p(k_shared), _p(cu_seqlens), _p(cu_seqlens_k), _p(out), _p(lse),
                                   _p(dout), _p(g["dq"]), _p(g["dk"]), _p(g["dv"]), _p(g["dk_shared"]), *dims, *strides,
                                   1 if causal else 0, q.shape[-1] ** -0.5 if scale is None else scale, _kda.KDA_BF16,
@@ -151,7 +167,7 @@ def latent_bwd(q, k, v, k_shared, out, lse, dout, cu_seqlens=None, cu_seqlens_k=
 
 
 def latent_decode_workspace_size(N, Tq, H) -> int:
-    return int(_kda.load().kda_latent_decode_workspace_size(N, Tq, H))
+    return _size("kda_latent_decode_workspace_size", N, Tq, H)
 
 
 def latent_decode_step(q, cache, page_table, seq_lens, scale=None, out=None, lse=None, workspace=None,
@@ -163,7 +179,7 @@ def latent_decode_step(q, cache, page_table, seq_lens, scale=None, out=None, lse
     third element when ``return_workspace``."""
     if q.dim() != 4 or cache.dim() != 3 or page_table.dim() != 2:
         raise ValueError("q must be [N, Tq, H, D], cache [pages, page_size, D], page_table [N, max_pages]")
-    dev = q.device
+    dev = q.get_device()
     N, Tq, H, W = q.shape
     pages, page = cache.shape[:2]
     _check("q", q, _BF16, dev)
@@ -171,15 +187,15 @@ def latent_decode_step(q, cache, page_table, seq_lens, scale=None, out=None, lse
     _check("page_table", page_table, _I32, dev, (N, page_table.shape[1]))
     _check("seq_lens", seq_lens, _I32, dev, (N,))
     if out is None:
-        out = torch.empty(N, Tq, H, LATENT_DIM, dtype=_BF16, device=dev)
+        out = q.new_empty((N, Tq, H, LATENT_DIM))
     else:
         _check("out", out, _BF16, dev, (N, Tq, H, LATENT_DIM))
     if lse is None:
-        lse = torch.empty(N, Tq, H, dtype=_F32, device=dev)
+        lse = q.new_empty((N, Tq, H), dtype=_F32)
     else:
         _check("lse", lse, _F32, dev, (N, Tq, H))
     dr = W - LATENT_DIM
-    ws = _workspace(workspace, _kda.load().kda_latent_decode_workspace_size(N, Tq, H), dev)
+    ws = _workspace(workspace, latent_decode_workspace_size(N, Tq, H), q)
     _call("kda_latent_decode_step", dev, (_p(q), _p(cache), _p(page_table), _p(seq_lens), _p(out), _p(lse), N, Tq, H,
                                           LATENT_DIM, dr, page, pages, page_table.shape[1],
                                           (HEAD_DIM + dr) ** -0.5 if scale is None else scale, _kda.KDA_BF16, _p(ws),
@@ -194,7 +210,7 @@ def latent_append(c, k_shared, cache, slots, weight=None, eps=1e-5):
     rows outside it, such as -1, are skipped). ``weight`` fp32 [512], or None for c as it is."""
     if c.dim() != 2 or cache.dim() != 3:
         raise ValueError("c must be [T, 512] and cache [pages, page_size, D]")
-    dev = c.device
+    dev = c.get_device()
     T, dr = c.shape[0], 0 if k_shared is None else k_shared.shape[-1]
     _check("c", c, _BF16, dev, dense=False)
     _check("cache", cache, _BF16, dev, (*cache.shape[:2], c.shape[1] + dr))
@@ -212,7 +228,7 @@ def latent_append(c, k_shared, cache, slots, weight=None, eps=1e-5):
 
 
 def _norm_args(x, weight, residual, residual_out):
-    dev = x.device
+    dev = x.get_device()
     D = x.shape[-1]
     if x.dtype not in (_F32, _BF16):
         raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
@@ -250,7 +266,7 @@ def rms_norm_e4m3(x, weight, residual=None, eps=1e-5, out=None, scale=None, resi
     else:
         _check("out", out, torch.float8_e4m3fn, dev, x.shape)
     if scale is None:
-        scale = torch.empty(*x.shape[:-1], D // 128, dtype=_F32, device=dev)
+        scale = x.new_empty((*x.shape[:-1], D // 128), dtype=_F32)
     else:
         _check("scale", scale, _F32, dev, (*x.shape[:-1], D // 128))
     _call("kda_rms_norm_e4m3", dev, (_p(x), _p(residual), _p(weight), _p(out), _p(scale), _p(h),
@@ -259,14 +275,14 @@ def rms_norm_e4m3(x, weight, residual=None, eps=1e-5, out=None, scale=None, resi
 
 
 def rms_norm_bwd_workspace_size(rows, D) -> int:
-    return int(_kda.load().kda_rms_norm_bwd_workspace_size(rows, D))
+    return _size("kda_rms_norm_bwd_workspace_size", rows, D)
 
 
 def rms_norm_bwd(dy, h, weight, dh=None, eps=1e-5, dx=None, dweight=None, workspace=None):
     """``kda_rms_norm_bwd``: gradients of ``rms_norm`` at its h: dy [..., D] the gradient of y, ``dh`` that of
     h along the residual stream (or None). Returns (dx, the gradient of x and of the residual, in h's dtype,
     and dweight fp32 [D])."""
-    dev, D = h.device, h.shape[-1]
+    dev, D = h.get_device(), h.shape[-1]
     if h.dtype not in (_F32, _BF16):
         raise TypeError("h must be float32 or bfloat16, got %s" % h.dtype)
     _check("h", h, h.dtype, dev)
@@ -279,11 +295,11 @@ def rms_norm_bwd(dy, h, weight, dh=None, eps=1e-5, dx=None, dweight=None, worksp
     else:
         _check("dx", dx, h.dtype, dev, h.shape)
     if dweight is None:
-        dweight = torch.empty(D, dtype=_F32, device=dev)
+        dweight = h.new_empty((D,), dtype=_F32)
     else:
         _check("dweight", dweight, _F32, dev, (D,))
     rows = h.numel() // D if D else 0
-    ws = _workspace(workspace, rms_norm_bwd_workspace_size(rows, D), dev)
+    ws = _workspace(workspace, rms_norm_bwd_workspace_size(rows, D), h)
     _call("kda_rms_norm_bwd", dev, (_p(dy), _p(h), _p(weight), _p(dh), _p(dx), _p(dweight), rows, D, eps,
                                     _kda._dtype_code(h), _p(ws), ws.numel()))
     return dx, dweight
