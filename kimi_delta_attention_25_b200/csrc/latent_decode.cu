@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb)
         l = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
         const int col = blockIdx.z * 32 + lane;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 20
         for (int s = warp; s < parts; s += 4) {
             const float f = s_f[s];
             const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(s, r) * kLatentDim) + col);

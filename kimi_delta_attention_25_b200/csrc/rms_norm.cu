@@ -172,45 +172,61 @@ struct NormBwdParams {
 };
 
 // TPR threads hold one row, and the block walks its rows with the weight gradient's sum in registers;
-// a second kernel adds the blocks' sums in a fixed order, so results do not depend on timing.
+// a second kernel adds the blocks' sums in a fixed order, so results do not depend on timing. With one vector
+// a thread (up to 1024 of them a row) the weights stay in registers too, and the next row is on its way while
+// this one is worked on (8192 x 4096 bf16: two vectors a thread and 1024 threads an SM took 56 us, this @N1@).
 template <typename T, int TPR, int VPT, bool DH>
 __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
 {
     constexpr int NV = Vec<T>::n;
+    constexpr bool AHEAD = VPT == 1;
     __shared__ float red[2][TPR / 32][2];
     const int t = threadIdx.x, nvec = p.D / NV;
-    float dw[VPT][NV];
+    float dw[VPT][NV], w1[AHEAD ? NV : 1];
+    auto weights = [&](int v, float *w) {
+#pragma unroll
+        for (int e = 0; e < NV; e += 4) {
+            const float4 w4 = v < nvec ? *reinterpret_cast<const float4 *>(p.w + (size_t)v * NV + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            w[e] = w4.x; w[e + 1] = w4.y; w[e + 2] = w4.z; w[e + 3] = w4.w;
+        }
+    };
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < NV; ++e) dw[i][e] = 0.f;
+    if constexpr (AHEAD) weights(t, w1);
+    auto fetch = [&](const void *src, long long row, int v) {
+        return row < p.rows && v < nvec ? __ldcs((const uint4 *)src + (size_t)row * nvec + v) : make_uint4(0, 0, 0, 0);
+    };
+    uint4 hn, gn, en = make_uint4(0, 0, 0, 0);
+    auto next = [&](long long row) {
+        hn = fetch(p.h, row, t);
+        gn = fetch(p.dy, row, t);
+        if constexpr (DH) en = fetch(p.dh, row, t);
+    };
+    if constexpr (AHEAD) next(blockIdx.x);
     int flip = 0;
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
-        const size_t base = (size_t)row * nvec;
-        uint4 hv[VPT], gv[VPT], ev[VPT];
+        uint4 hv[VPT], gv[VPT], ev = en;
+        if constexpr (AHEAD) {
+            hv[0] = hn; gv[0] = gn;
+            next(row + gridDim.x);
+        } else {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = i * TPR + t;
-            hv[i] = gv[i] = ev[i] = make_uint4(0, 0, 0, 0);
-            if (v < nvec) {
-                hv[i] = __ldcs((const uint4 *)p.h + base + v);
-                gv[i] = __ldcs((const uint4 *)p.dy + base + v);
-                if constexpr (DH) ev[i] = __ldcs((const uint4 *)p.dh + base + v);
-            }
+            for (int i = 0; i < VPT; ++i) { hv[i] = fetch(p.h, row, i * TPR + t); gv[i] = fetch(p.dy, row, i * TPR + t); }
         }
         float ss = 0.f, sg = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = i * TPR + t;
-            float h[NV], g[NV];
+            float h[NV], g[NV], wl[NV];
             Vec<T>::unpack(hv[i], h);
             Vec<T>::unpack(gv[i], g);
+            if constexpr (!AHEAD) weights(i * TPR + t, wl);
+            const float *w = AHEAD ? w1 : wl;
 #pragma unroll
-            for (int e = 0; e < NV; e += 4) {
-                const float4 w = v < nvec ? *reinterpret_cast<const float4 *>(p.w + (size_t)v * NV + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-                ss += h[e] * h[e]; ss += h[e + 1] * h[e + 1]; ss += h[e + 2] * h[e + 2]; ss += h[e + 3] * h[e + 3];
-                sg += g[e] * w.x * h[e]; sg += g[e + 1] * w.y * h[e + 1];
-                sg += g[e + 2] * w.z * h[e + 2]; sg += g[e + 3] * w.w * h[e + 3];
+            for (int e = 0; e < NV; ++e) {
+                ss += h[e] * h[e];
+                sg += g[e] * w[e] * h[e];
             }
         }
 #pragma unroll
@@ -224,27 +240,25 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
             ss = red[flip][0][0];
             sg = red[flip][0][1];
 #pragma unroll
-            for (int w = 1; w < TPR / 32; ++w) { ss += red[flip][w][0]; sg += red[flip][w][1]; }
+            for (int x = 1; x < TPR / 32; ++x) { ss += red[flip][x][0]; sg += red[flip][x][1]; }
         }
         const float r = 1.f / sqrtf(ss * p.inv_d + p.eps), c = r * r * (sg * p.inv_d);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = i * TPR + t;
-            float h[NV], g[NV], d[NV];
+            float h[NV], g[NV], d[NV], wl[NV];
             Vec<T>::unpack(hv[i], h);
             Vec<T>::unpack(gv[i], g);
-            Vec<T>::unpack(ev[i], d);
+            if constexpr (DH && !AHEAD) ev = fetch(p.dh, row, v);
+            Vec<T>::unpack(ev, d);
+            if constexpr (!AHEAD) weights(v, wl);
+            const float *w = AHEAD ? w1 : wl;
 #pragma unroll
-            for (int e = 0; e < NV; e += 4) {
-                const float4 w4 = v < nvec ? *reinterpret_cast<const float4 *>(p.w + (size_t)v * NV + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-                const float w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    dw[i][e + u] += g[e + u] * (h[e + u] * r);
-                    d[e + u] += r * (g[e + u] * w[u] - h[e + u] * c);
-                }
+            for (int e = 0; e < NV; ++e) {
+                dw[i][e] += g[e] * (h[e] * r);
+                d[e] += r * (g[e] * w[e] - h[e] * c);
             }
-            if (v < nvec) ((uint4 *)p.dx)[base + v] = Vec<T>::pack(d);
+            if (v < nvec) ((uint4 *)p.dx)[(size_t)row * nvec + v] = Vec<T>::pack(d);
         }
     }
 #pragma unroll
@@ -259,24 +273,23 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
     }
 }
 
-// dw[c] = sum over blocks of partial[block][c]: 32 channels per CTA, 8 warps over the blocks.
-__global__ void __launch_bounds__(256) rms_norm_dw_kernel(const float *__restrict__ partial, float *__restrict__ dw,
-                                                          int blocks, int D)
+// dw[c] = sum over blocks of partial[block][c]: 32 channels per CTA, 32 warps over the blocks.
+__global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float *__restrict__ partial, float *__restrict__ dw,
+                                                           int blocks, int D)
 {
-    __shared__ float s[8][32];
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float a = 0.f;
     if (c < D) {
-#pragma unroll 4
-        for (int b = warp; b < blocks; b += 8) a += partial[(size_t)b * D + c];
+#pragma unroll 16
+        for (int b = warp; b < blocks; b += 32) a += partial[(size_t)b * D + c];
     }
     s[warp][lane] = a;
     __syncthreads();
-    if (warp == 0 && c < D) {
+    a = s[lane][warp];                        // channel `warp` of the CTA, over the 32 sums
 #pragma unroll
-        for (int w = 1; w < 8; ++w) a += s[w][lane];
-        dw[c] = a;
-    }
+    for (int m = 16; m > 0; m >>= 1) a += __shfl_xor_sync(0xffffffffu, a, m);
+    if (lane == 0 && blockIdx.x * 32 + warp < D) dw[blockIdx.x * 32 + warp] = a;
 }
 
 // One warp per token: 16 of the 512 latent channels per lane (two vectors), then the shared key part.
@@ -363,17 +376,26 @@ kda_status_t run_norm(const void *x, const void *residual, const float *weight, 
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-// Blocks of the backward pass: a function of the sizes alone, as the workspace holds their sums.
-int bwd_blocks(long long rows) { return (int)(rows < 592 ? (rows > 0 ? rows : 1) : 592); }
+// Threads that hold a row of the backward pass, and its blocks: 1024 threads on each of 148 SMs.
+int bwd_threads(int nvec)
+{
+    return nvec <= 32 ? 32 : nvec <= 128 ? 128 : nvec <= 256 ? 256 : nvec <= 512 ? 512 : nvec <= 1024 ? 1024 : 512;
+}
+int bwd_blocks(long long rows, int nvec)
+{
+    const long long most = 148 * 1024 / bwd_threads(nvec);
+    return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
+}
 
 template <typename T, bool DH>
 void launch_norm_bwd(const NormBwdParams &p, int blocks, cudaStream_t st)
 {
     const int nvec = p.D / Vec<T>::n;
-    if (nvec <= 32 * 2) rms_norm_bwd_kernel<T, 32, 2, DH><<<blocks, 32, 0, st>>>(p);
-    else if (nvec <= 128 * 2) rms_norm_bwd_kernel<T, 128, 2, DH><<<blocks, 128, 0, st>>>(p);
-    else if (nvec <= 256 * 2) rms_norm_bwd_kernel<T, 256, 2, DH><<<blocks, 256, 0, st>>>(p);
-    else if (nvec <= 512 * 2) rms_norm_bwd_kernel<T, 512, 2, DH><<<blocks, 512, 0, st>>>(p);
+    if (nvec <= 32) rms_norm_bwd_kernel<T, 32, 1, DH><<<blocks, 32, 0, st>>>(p);
+    else if (nvec <= 128) rms_norm_bwd_kernel<T, 128, 1, DH><<<blocks, 128, 0, st>>>(p);
+    else if (nvec <= 256) rms_norm_bwd_kernel<T, 256, 1, DH><<<blocks, 256, 0, st>>>(p);
+    else if (nvec <= 512) rms_norm_bwd_kernel<T, 512, 1, DH><<<blocks, 512, 0, st>>>(p);
+    else if (nvec <= 1024) rms_norm_bwd_kernel<T, 1024, 1, DH><<<blocks, 1024, 0, st>>>(p);
     else if (nvec <= 512 * 4) rms_norm_bwd_kernel<T, 512, 4, DH><<<blocks, 512, 0, st>>>(p);
     else rms_norm_bwd_kernel<T, 512, 8, DH><<<blocks, 512, 0, st>>>(p);
 }
@@ -400,7 +422,8 @@ kda_status_t kda_rms_norm_e4m3(const void *x, const void *residual, const float 
 size_t kda_rms_norm_bwd_workspace_size(long long rows, int D)
 {
     if (rows < 0 || rows > 0x7fffffffLL || D <= 0 || D % 8 != 0 || D > kNormMaxWidth) return 0;
-    return (size_t)bwd_blocks(rows) * D * sizeof(float);
+    const int a = bwd_blocks(rows, D / 8), b = bwd_blocks(rows, D / 4);      // bf16, fp32
+    return (size_t)(a > b ? a : b) * D * sizeof(float);
 }
 
 kda_status_t kda_rms_norm_bwd(const void *dy, const void *h, const float *weight, const void *dh, void *dx,
@@ -420,12 +443,12 @@ kda_status_t kda_rms_norm_bwd(const void *dy, const void *h, const float *weight
     NormBwdParams p;
     p.dy = dy; p.h = h; p.dh = dh; p.w = weight; p.dx = dx; p.partial = (float *)workspace; p.eps = eps;
     p.inv_d = 1.f / (float)D; p.rows = rows; p.D = D;
-    const int blocks = bwd_blocks(rows);
+    const int blocks = bwd_blocks(rows, dtype == KDA_BF16 ? D / 8 : D / 4);
     using bf = __nv_bfloat16;
     if (dtype == KDA_BF16) dh ? launch_norm_bwd<bf, true>(p, blocks, st) : launch_norm_bwd<bf, false>(p, blocks, st);
     else dh ? launch_norm_bwd<float, true>(p, blocks, st) : launch_norm_bwd<float, false>(p, blocks, st);
     if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
-    rms_norm_dw_kernel<<<(D + 31) / 32, 256, 0, st>>>(p.partial, dweight, blocks, D);
+    rms_norm_dw_kernel<<<(D + 31) / 32, 1024, 0, st>>>(p.partial, dweight, blocks, D);
     return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
