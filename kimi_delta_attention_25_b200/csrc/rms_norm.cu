@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include "kda_internal.cuh"
+#include "sm100.cuh"
 
 namespace kda {
 namespace {
@@ -171,17 +172,29 @@ struct NormBwdParams {
     int D;
 };
 
+__device__ __forceinline__ void bulk_row(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(sm100::smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(sm100::smem_u32(bar)) : "memory");
+}
+
 // TPR threads hold one row, and the block walks its rows with the weight gradient's sum in registers;
-// a second kernel adds the blocks' sums in a fixed order, so results do not depend on timing. With one vector
-// a thread (up to 1024 of them a row) the weights stay in registers too, and the next row is on its way while
-// this one is worked on (8192 x 4096 bf16: two vectors a thread and 1024 threads an SM took 56 us, this @N1@).
+// a second kernel adds the blocks' sums in a fixed order, so results do not depend on timing. Up to 1024 vectors
+// a row (one a thread) the rows come through shared memory, kRowsAhead of them by bulk copies of one thread, which
+// keeps 190 KB an SM on their way without a register (8192 x 4096 bf16: rows loaded into registers one ahead took
+// 55 us, this 45); wider rows are loaded as they are needed.
+constexpr int kRowsAhead = 4;
 template <typename T, int TPR, int VPT, bool DH>
 __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
 {
     constexpr int NV = Vec<T>::n;
     constexpr bool AHEAD = VPT == 1;
+    extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float red[2][TPR / 32][2];
+    __shared__ uint64_t full[kRowsAhead];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t = threadIdx.x, nvec = p.D / NV;
+    const uint32_t row_bytes = (uint32_t)nvec * 16;
     float dw[VPT][NV], w1[AHEAD ? NV : 1];
     auto weights = [&](int v, float *w) {
 #pragma unroll
@@ -194,23 +207,42 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int e = 0; e < NV; ++e) dw[i][e] = 0.f;
-    if constexpr (AHEAD) weights(t, w1);
     auto fetch = [&](const void *src, long long row, int v) {
-        return row < p.rows && v < nvec ? __ldcs((const uint4 *)src + (size_t)row * nvec + v) : make_uint4(0, 0, 0, 0);
+        return v < nvec ? __ldcs((const uint4 *)src + (size_t)row * nvec + v) : make_uint4(0, 0, 0, 0);
     };
-    uint4 hn, gn, en = make_uint4(0, 0, 0, 0);
-    auto next = [&](long long row) {
-        hn = fetch(p.h, row, t);
-        gn = fetch(p.dy, row, t);
-        if constexpr (DH) en = fetch(p.dh, row, t);
+    auto order = [&](long long row, int s) {                  // one thread: the row's tensors into stage s
+        if (row >= p.rows) return;
+        unsigned char *dst = ring + (size_t)s * (DH ? 3 : 2) * row_bytes;
+        sm100::mbar_arrive_expect_tx(&full[s], (DH ? 3 : 2) * row_bytes);
+        bulk_row(dst, (const unsigned char *)p.h + (size_t)row * row_bytes, row_bytes, &full[s]);
+        bulk_row(dst + row_bytes, (const unsigned char *)p.dy + (size_t)row * row_bytes, row_bytes, &full[s]);
+        if constexpr (DH) bulk_row(dst + 2 * row_bytes, (const unsigned char *)p.dh + (size_t)row * row_bytes, row_bytes, &full[s]);
     };
-    if constexpr (AHEAD) next(blockIdx.x);
-    int flip = 0;
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
-        uint4 hv[VPT], gv[VPT], ev = en;
+    if constexpr (AHEAD) {
+        if (t == 0) {
+            for (int s = 0; s < kRowsAhead; ++s) sm100::mbar_init(&full[s], 1);
+            sm100::fence_mbar_init();
+        }
+        __syncthreads();
+        if (t == 0)
+            for (int s = 0; s < kRowsAhead; ++s) order(blockIdx.x + (long long)s * gridDim.x, s);
+        weights(t, w1);
+    }
+    int it = 0;
+    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, ++it) {
+        const int flip = it & 1, stage = it % kRowsAhead;
+        uint4 hv[VPT], gv[VPT], ev = make_uint4(0, 0, 0, 0);
         if constexpr (AHEAD) {
-            hv[0] = hn; gv[0] = gn;
-            next(row + gridDim.x);
+            // (a copy that did not come within two seconds leaves what the stage holds: a device fault, which the
+            // next call reports)
+            sm100::mbar_wait(&full[stage], (it / kRowsAhead) & 1);
+            const uint4 *src = reinterpret_cast<const uint4 *>(ring + (size_t)stage * (DH ? 3 : 2) * row_bytes);
+            hv[0] = gv[0] = make_uint4(0, 0, 0, 0);
+            if (t < nvec) {
+                hv[0] = src[t];
+                gv[0] = src[nvec + t];
+                if constexpr (DH) ev = src[2 * nvec + t];
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) { hv[i] = fetch(p.h, row, i * TPR + t); gv[i] = fetch(p.dy, row, i * TPR + t); }
@@ -234,9 +266,16 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
             ss += __shfl_xor_sync(0xffffffffu, ss, m);
             sg += __shfl_xor_sync(0xffffffffu, sg, m);
         }
-        if constexpr (TPR > 32) {             // two buffers in turn: one barrier a row is enough
+        // two buffers in turn: one barrier a row is enough; behind it every thread has read the row's stage
+        if constexpr (TPR > 32) {
             if ((t & 31) == 0) { red[flip][t >> 5][0] = ss; red[flip][t >> 5][1] = sg; }
             __syncthreads();
+        } else {
+            __syncwarp();
+        }
+        if constexpr (AHEAD)
+            if (t == 0) order(row + (long long)kRowsAhead * gridDim.x, stage);
+        if constexpr (TPR > 32) {
             ss = red[flip][0][0];
             sg = red[flip][0][1];
 #pragma unroll
@@ -280,6 +319,7 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float *__restri
     __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float a = 0.f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c < D) {
 #pragma unroll 16
         for (int b = warp; b < blocks; b += 32) a += partial[(size_t)b * D + c];
@@ -388,16 +428,26 @@ int bwd_blocks(long long rows, int nvec)
 }
 
 template <typename T, bool DH>
-void launch_norm_bwd(const NormBwdParams &p, int blocks, cudaStream_t st)
+cudaError_t launch_norm_bwd(const NormBwdParams &p, int blocks, cudaStream_t st)
 {
     const int nvec = p.D / Vec<T>::n;
-    if (nvec <= 32) rms_norm_bwd_kernel<T, 32, 1, DH><<<blocks, 32, 0, st>>>(p);
-    else if (nvec <= 128) rms_norm_bwd_kernel<T, 128, 1, DH><<<blocks, 128, 0, st>>>(p);
-    else if (nvec <= 256) rms_norm_bwd_kernel<T, 256, 1, DH><<<blocks, 256, 0, st>>>(p);
-    else if (nvec <= 512) rms_norm_bwd_kernel<T, 512, 1, DH><<<blocks, 512, 0, st>>>(p);
-    else if (nvec <= 1024) rms_norm_bwd_kernel<T, 1024, 1, DH><<<blocks, 1024, 0, st>>>(p);
-    else if (nvec <= 512 * 4) rms_norm_bwd_kernel<T, 512, 4, DH><<<blocks, 512, 0, st>>>(p);
-    else rms_norm_bwd_kernel<T, 512, 8, DH><<<blocks, 512, 0, st>>>(p);
+    const int ring = nvec <= 1024 ? kRowsAhead * (DH ? 3 : 2) * nvec * 16 : 0;
+    auto go = [&](auto kern, int threads) {
+        if (ring > 32 * 1024) {               // (48 KB, the static part among them, need no leave)
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+            if (e != cudaSuccess) return e;
+        }
+        kern<<<blocks, threads, ring, st>>>(p);
+        return cudaGetLastError();
+    };
+    if (nvec <= 32) return go(rms_norm_bwd_kernel<T, 32, 1, DH>, 32);
+    if (nvec <= 128) return go(rms_norm_bwd_kernel<T, 128, 1, DH>, 128);
+    if (nvec <= 256) return go(rms_norm_bwd_kernel<T, 256, 1, DH>, 256);
+    if (nvec <= 512) return go(rms_norm_bwd_kernel<T, 512, 1, DH>, 512);
+    if (nvec <= 1024) return go(rms_norm_bwd_kernel<T, 1024, 1, DH>, 1024);
+    if constexpr (Vec<T>::n == 4)
+        if (nvec > 512 * 4) return go(rms_norm_bwd_kernel<T, 512, 8, DH>, 512);
+    return go(rms_norm_bwd_kernel<T, 512, 4, DH>, 512);
 }
 
 }  // namespace
@@ -445,11 +495,21 @@ kda_status_t kda_rms_norm_bwd(const void *dy, const void *h, const float *weight
     p.inv_d = 1.f / (float)D; p.rows = rows; p.D = D;
     const int blocks = bwd_blocks(rows, dtype == KDA_BF16 ? D / 8 : D / 4);
     using bf = __nv_bfloat16;
-    if (dtype == KDA_BF16) dh ? launch_norm_bwd<bf, true>(p, blocks, st) : launch_norm_bwd<bf, false>(p, blocks, st);
-    else dh ? launch_norm_bwd<float, true>(p, blocks, st) : launch_norm_bwd<float, false>(p, blocks, st);
-    if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
-    rms_norm_dw_kernel<<<(D + 31) / 32, 1024, 0, st>>>(p.partial, dweight, blocks, D);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const cudaError_t e = dtype == KDA_BF16 ? (dh ? launch_norm_bwd<bf, true>(p, blocks, st) : launch_norm_bwd<bf, false>(p, blocks, st))
+                                            : (dh ? launch_norm_bwd<float, true>(p, blocks, st) : launch_norm_bwd<float, false>(p, blocks, st));
+    if (e != cudaSuccess) return KDA_ERR_CUDA;
+    // scheduled while the first kernel's last rows are worked on; it waits for all of them
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((D + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    const float *partial = p.partial;
+    return cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel, partial, dweight, blocks, D) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status_t kda_latent_append(const void *c, const void *k_shared, const long long *slots, const float *weight,
