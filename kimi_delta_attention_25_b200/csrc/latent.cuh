@@ -47,20 +47,25 @@ __device__ __forceinline__ int latent_sequence(const int32_t *cu, int N, int T, 
 
 // Tile c of sequence n over offsets `cu` (rows of `tile`) has slot floor(first row / tile) + n + c: unique, and
 // below total / tile + N. The inverse: the sequence and the tile's first row within it; false for a slot that no
-// tile uses, and for offsets that lie outside the tensors.
+// tile uses, and for offsets that lie outside the tensors. Called by whole warps.
 __device__ __forceinline__ bool latent_slot(const int32_t *cu, const LatentArgs &a, int L, bool keys, int tile, long long slot,
                                             int *n, LatentSpan *s, long long *row)
 {
-    int lo = 0, hi = a.N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        const long long st = cu ? (long long)cu[mid] : (long long)mid * L;
-        if (st / tile + mid <= slot) lo = mid; else hi = mid - 1;
+    // the last sequence whose first slot is not behind `slot`: the warp's lanes ask for 32 of them at a time
+    const int lane = threadIdx.x & 31;
+    int lo = 0, count = a.N;
+    while (count > 1) {
+        const int step = (count + 31) / 32, at = lo + lane * step;
+        const long long st = at < lo + count ? (cu ? (long long)cu[at] : (long long)at * L) : 0;
+        const uint32_t before = __ballot_sync(0xffffffffu, at < lo + count && st / tile + at <= slot);
+        const int i = before ? 31 - __clz(before) : 0;         // offsets that decrease give some sequence, checked below
+        count = min(step, count - i * step);
+        lo += i * step;
     }
     if (!latent_span(a.cu_q, a.cu_k, lo, a.T, a.Tk, s)) return false;
-    const long long first = keys ? s->k0 : s->q0, count = keys ? s->k1 - s->k0 : s->q1 - s->q0;
+    const long long first = keys ? s->k0 : s->q0, rows = keys ? s->k1 - s->k0 : s->q1 - s->q0;
     const long long c = slot - (first / tile + lo);
-    if (c < 0 || c * tile >= count) return false;
+    if (c < 0 || c * tile >= rows) return false;
     *n = lo;
     *row = c * tile;
     return true;

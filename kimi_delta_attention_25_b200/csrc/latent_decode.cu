@@ -568,7 +568,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
 // status word.
 constexpr int kManyParts = 8;
 template <int RG>
-__global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb)
+__global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb, int by_share)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int cut = blockIdx.x / a.G, g = blockIdx.x % a.G, t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -578,27 +578,32 @@ __global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb)
         err = __syncthreads_or(err == KDA_ERR_TIMEOUT) ? KDA_ERR_TIMEOUT : (__syncthreads_or(err) ? KDA_ERR_INVALID_ARG : 0);
         if (t == 0) *a.status = err;
     }
-    // the share at whose end the cut-th cut sequence begins
+    // the share at whose end the cut-th cut sequence begins; with `by_share` (as many sequences as shares, or nearly)
+    // block x looks at its own share instead of counting cuts
     __shared__ int s_cut[4], s_found;
     __shared__ float4 s_o[4][32];
-    int before = 0, share = -1;
-    if (t == 0) s_found = -1;
-    for (int base = 0; base < a.L; base += 128) {
-        const int i = base + t;
-        const bool is = i < a.L && a.meta[2 * i] >= 0;
-        const uint32_t ball = __ballot_sync(0xffffffffu, is);
-        if (lane == 0) s_cut[warp] = __popc(ball);
-        __syncthreads();
-        int at = before + __popc(ball & ((1u << lane) - 1));
-        for (int w = 0; w < 4; ++w) { if (w < warp) at += s_cut[w]; before += s_cut[w]; }
-        if (is && at == cut) s_found = i;
-        __syncthreads();
+    int share = by_share ? cut : -1;
+    if (!by_share) {
+        int before = 0;
+        if (t == 0) s_found = -1;
+        for (int base = 0; base < a.L; base += 128) {
+            const int i = base + t;
+            const bool is = i < a.L && a.meta[2 * i] >= 0;
+            const uint32_t ball = __ballot_sync(0xffffffffu, is);
+            if (lane == 0) s_cut[warp] = __popc(ball);
+            __syncthreads();
+            int at = before + __popc(ball & ((1u << lane) - 1));
+            for (int w = 0; w < 4; ++w) { if (w < warp) at += s_cut[w]; before += s_cut[w]; }
+            if (is && at == cut) s_found = i;
+            __syncthreads();
+        }
+        share = s_found;
     }
-    share = s_found;
-    if (share < 0) return;
+    if (share < 0 || a.meta[2 * share] < 0) return;
     const int n = a.meta[2 * share], last = a.meta[2 * share + 1], parts = last - share + 1;
     const bool many = parts > kManyParts;
     if (!many && blockIdx.z > 0) return;
+    const int quarters = 4 / gridDim.z;                        // of the channels, for this block, with many parts
     auto slot_of = [&](int s, int r) { return ((size_t)((share + s) * a.G + g) * 2 + (s == 0 ? 1 : 0)) * RG + r; };
     const int r_end = min(min(RG, a.Tq * a.H - g * RG), ((int)blockIdx.y + 1) * rpb);
     const size_t row0 = (size_t)n * a.Tq * a.H + g * RG;
@@ -656,25 +661,27 @@ __global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb)
         if (lane == 0) s_red[1][warp] = l;
         __syncthreads();
         l = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
-        const int col = blockIdx.z * 32 + lane;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int qt = 0; qt < quarters; ++qt) {
+            const int col = (blockIdx.z * quarters + qt) * 32 + lane;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 20
-        for (int s = warp; s < parts; s += 4) {
-            const float f = s_f[s];
-            const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(s, r) * kLatentDim) + col);
-            o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
-        }
-        s_o[warp][lane] = o;
-        __syncthreads();
-        if (warp == 0) {
+            for (int s = warp; s < parts; s += 4) {
+                const float f = s_f[s];
+                const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(s, r) * kLatentDim) + col);
+                o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+            }
+            s_o[warp][lane] = o;
+            __syncthreads();
+            if (warp == 0) {
 #pragma unroll
-            for (int w = 1; w < 4; ++w) { const float4 x = s_o[w][lane]; o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w; }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            reinterpret_cast<uint2 *>(a.out + (row0 + r) * kLatentDim)[col] =
-                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-            if (col == 0) a.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                for (int w = 1; w < 4; ++w) { const float4 x = s_o[w][lane]; o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w; }
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                reinterpret_cast<uint2 *>(a.out + (row0 + r) * kLatentDim)[col] =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                if (col == 0) a.lse[row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -711,14 +718,15 @@ cudaError_t launch(const DecodeArgs &a, const CUtensorMap &tq, const CUtensorMap
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    // at most one cut a share and one a sequence; with few of them a block per row, else four rows to a block
-    const int cuts = a.N < a.L ? a.N : a.L, rows = RG < a.Tq * a.H ? RG : a.Tq * a.H, rpb = cuts * a.G <= 8 ? 1 : 4;
-    cfg.gridDim = dim3(cuts * a.G, (rows + rpb - 1) / rpb, 4);
+    // at most one cut a share and one a sequence; with few of them a block per row and quarter, else four rows to a block
+    const int by_share = 2 * a.N >= a.L, cuts = by_share ? a.L : a.N, rows = RG < a.Tq * a.H ? RG : a.Tq * a.H;
+    const int rpb = cuts * a.G <= 8 ? 1 : 4;
+    cfg.gridDim = dim3(cuts * a.G, (rows + rpb - 1) / rpb, by_share ? 1 : 4);
     cfg.blockDim = dim3(128);
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_decode_join<RG>, a, rpb);
+    return cudaLaunchKernelEx(&cfg, latent_decode_join<RG>, a, rpb, by_share);
 }
 
 }  // namespace
