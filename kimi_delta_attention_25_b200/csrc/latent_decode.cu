@@ -563,37 +563,37 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
 
 // Joins the partial results of each sequence that a cut runs through. Block (cut, rows of a group, quarter of
 // the channels) with `rpb` rows. A sequence with many parts takes the whole block to a row and quarter, each warp
-// adding every fourth part; one with few parts takes a warp to a row, all of its channels, in the blocks of the
+// adding every NW-th part; one with few parts takes a warp to a row, all of its channels, in the blocks of the
 // first quarter. The sums are added in a fixed order. The first block also gathers the blocks' errors into the
 // status word.
 constexpr int kManyParts = 8;
-template <int RG>
-__global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb, int by_share)
+template <int RG, int NW>
+__global__ void __launch_bounds__(32 * NW) latent_decode_join(DecodeArgs a, int rpb, int by_share)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int cut = blockIdx.x / a.G, g = blockIdx.x % a.G, t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
         int err = 0;
-        for (int i = t; i < a.L * a.G; i += 128) err = max(err, a.errs[i]);
+        for (int i = t; i < a.L * a.G; i += 32 * NW) err = max(err, a.errs[i]);
         err = __syncthreads_or(err == KDA_ERR_TIMEOUT) ? KDA_ERR_TIMEOUT : (__syncthreads_or(err) ? KDA_ERR_INVALID_ARG : 0);
         if (t == 0) *a.status = err;
     }
     // the share at whose end the cut-th cut sequence begins; with `by_share` (as many sequences as shares, or nearly)
     // block x looks at its own share instead of counting cuts
-    __shared__ int s_cut[4], s_found;
-    __shared__ float4 s_o[4][32];
+    __shared__ int s_cut[NW], s_found;
+    __shared__ float4 s_o[NW][32];
     int share = by_share ? cut : -1;
     if (!by_share) {
         int before = 0;
         if (t == 0) s_found = -1;
-        for (int base = 0; base < a.L; base += 128) {
+        for (int base = 0; base < a.L; base += 32 * NW) {
             const int i = base + t;
             const bool is = i < a.L && a.meta[2 * i] >= 0;
             const uint32_t ball = __ballot_sync(0xffffffffu, is);
             if (lane == 0) s_cut[warp] = __popc(ball);
             __syncthreads();
             int at = before + __popc(ball & ((1u << lane) - 1));
-            for (int w = 0; w < 4; ++w) { if (w < warp) at += s_cut[w]; before += s_cut[w]; }
+            for (int w = 0; w < NW; ++w) { if (w < warp) at += s_cut[w]; before += s_cut[w]; }
             if (is && at == cut) s_found = i;
             __syncthreads();
         }
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb,
     const int r_end = min(min(RG, a.Tq * a.H - g * RG), ((int)blockIdx.y + 1) * rpb);
     const size_t row0 = (size_t)n * a.Tq * a.H + g * RG;
     if (!many) {
-        for (int r = blockIdx.y * rpb + warp; r < r_end; r += 4) {
+        for (int r = blockIdx.y * rpb + warp; r < r_end; r += NW) {
             float2 ml = make_float2(-INFINITY, 0.f);
             if (lane < parts) ml = *reinterpret_cast<const float2 *>(a.part_ml + slot_of(lane, r) * 2);
             const float m = warp_max(ml.x), f = ex2(ml.x - (m == -INFINITY ? 0.f : m));
@@ -636,36 +636,40 @@ __global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb,
         }
         return;
     }
-    __shared__ float s_f[kLanes], s_red[2][4];
+    constexpr int PT = (kLanes + 32 * NW - 1) / (32 * NW);     // parts of a thread
+    __shared__ float s_f[kLanes], s_red[2][NW];
     for (int r = blockIdx.y * rpb; r < r_end; ++r) {
-        float2 ml[2];
+        float2 ml[PT];
         float m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < PT; ++i) {
             ml[i] = make_float2(-INFINITY, 0.f);
-            if (t + 128 * i < parts) ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + slot_of(t + 128 * i, r) * 2);
+            if (t + 32 * NW * i < parts) ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + slot_of(t + 32 * NW * i, r) * 2);
             m = fmaxf(m, ml[i].x);
         }
         m = warp_max(m);
         if (lane == 0) s_red[0][warp] = m;
         __syncthreads();
-        m = fmaxf(fmaxf(s_red[0][0], s_red[0][1]), fmaxf(s_red[0][2], s_red[0][3]));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int w = 0; w < NW; ++w) m = fmaxf(m, s_red[0][w]);
+#pragma unroll
+        for (int i = 0; i < PT; ++i) {
             const float f = ex2(ml[i].x - (m == -INFINITY ? 0.f : m));
             l += f * ml[i].y;
-            if (t + 128 * i < parts) s_f[t + 128 * i] = f;
+            if (t + 32 * NW * i < parts) s_f[t + 32 * NW * i] = f;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
         if (lane == 0) s_red[1][warp] = l;
         __syncthreads();
-        l = (s_red[1][0] + s_red[1][1]) + (s_red[1][2] + s_red[1][3]);
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) l += s_red[1][w];
         for (int qt = 0; qt < quarters; ++qt) {
             const int col = (blockIdx.z * quarters + qt) * 32 + lane;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 20
-            for (int s = warp; s < parts; s += 4) {
+#pragma unroll 10
+            for (int s = warp; s < parts; s += NW) {
                 const float f = s_f[s];
                 const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(s, r) * kLatentDim) + col);
                 o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
@@ -674,7 +678,7 @@ __global__ void __launch_bounds__(128) latent_decode_join(DecodeArgs a, int rpb,
             __syncthreads();
             if (warp == 0) {
 #pragma unroll
-                for (int w = 1; w < 4; ++w) { const float4 x = s_o[w][lane]; o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w; }
+                for (int w = 1; w < NW; ++w) { const float4 x = s_o[w][lane]; o.x += x.x; o.y += x.y; o.z += x.z; o.w += x.w; }
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 reinterpret_cast<uint2 *>(a.out + (row0 + r) * kLatentDim)[col] =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -722,11 +726,12 @@ cudaError_t launch(const DecodeArgs &a, const CUtensorMap &tq, const CUtensorMap
     const int by_share = 2 * a.N >= a.L, cuts = by_share ? a.L : a.N, rows = RG < a.Tq * a.H ? RG : a.Tq * a.H;
     const int rpb = cuts * a.G <= 8 ? 1 : 4;
     cfg.gridDim = dim3(cuts * a.G, (rows + rpb - 1) / rpb, by_share ? 1 : 4);
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(by_share ? 128 : 512);
     cfg.stream = st;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, latent_decode_join<RG>, a, rpb, by_share);
+    return by_share ? cudaLaunchKernelEx(&cfg, latent_decode_join<RG, 4>, a, rpb, by_share)
+                    : cudaLaunchKernelEx(&cfg, latent_decode_join<RG, 16>, a, rpb, by_share);
 }
 
 }  // namespace
