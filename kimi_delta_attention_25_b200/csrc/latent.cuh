@@ -71,6 +71,46 @@ __device__ __forceinline__ bool latent_slot(const int32_t *cu, const LatentArgs 
     return true;
 }
 
+// The query tile (of `tile` rows) whose row of key tiles is the rank-th longest, of packed sequences, where the slots'
+// order says nothing about it: with few blocks to an SM the last ones should be the shortest (9 sequences of some 300
+// queries behind histories, 16 heads: 88 us in slot order, 75 so). Every block counts for itself, so only up to
+// kRankedSlots slots, behind which there are blocks enough to even it out. All of the block's threads; `scratch` is
+// shared memory for 2 slots + 1 integers, which the caller may use again when this returns (bulk copies: behind a
+// proxy fence).
+constexpr int kRankedSlots = 384;
+__device__ __forceinline__ bool latent_ranked(const LatentArgs &a, int tile, int slots, int rank, int *scratch, LatentSpan *s,
+                                              long long *row)
+{
+    int *work = scratch, *seq = scratch + slots, *found = seq + slots;
+    for (int i = threadIdx.x; i < slots; i += blockDim.x) work[i] = -1;
+    if (threadIdx.x == 0) *found = -1;
+    __syncthreads();
+    for (int n = threadIdx.x; n < a.N; n += blockDim.x) {
+        LatentSpan x;
+        if (!latent_span(a.cu_q, a.cu_k, n, a.T, a.Tk, &x)) continue;
+        const long long Lq = x.q1 - x.q0, Lk = x.k1 - x.k0;
+        for (long long c = 0; c * tile < Lq; ++c) {
+            const long long i = x.q0 / tile + n + c, keys = a.causal ? min(Lk, min((c + 1) * tile, Lq) + Lk - Lq) : Lk;
+            if (i < slots) { work[i] = keys > 0 ? (int)((keys + 127) / 128) : 0; seq[i] = n; }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < slots; i += blockDim.x) {
+        const int w = work[i];
+        int r = 0;
+        if (w >= 0) {
+            for (int j = 0; j < slots; ++j) r += work[j] > w || (work[j] == w && j < i);
+            if (r == rank) *found = i;
+        }
+    }
+    __syncthreads();
+    const int slot = *found, n = slot >= 0 ? seq[slot] : 0;
+    __syncthreads();
+    if (slot < 0 || !latent_span(a.cu_q, a.cu_k, n, a.T, a.Tk, s)) return false;
+    *row = (slot - (s->q0 / tile + n)) * tile;
+    return *row >= 0 && *row < s->q1 - s->q0;
+}
+
 // Records offsets that break the contract (cu[0] = 0, non-decreasing, cu[N] = T). One block's threads.
 __device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T, int32_t *status)
 {

@@ -81,15 +81,11 @@ struct GradMaps { CUtensorMap a1, a1r, a2, b1, b1r, b2; };   // dq: q, -, dout, 
 // While dS(j) is formed from dP(j), S(j + 1) runs; while P(j + 1) is formed from it, the accumulating product of
 // tile j and dP(j + 1) do. The units of B1 are freed one by one by the accumulation.
 template <bool DQ>
-__device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdArgs &b, long long slot, int h, const GradMaps &maps,
-                                           unsigned char *sm)
+__device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdArgs &b, const LatentSpan &sp, long long r0, int h,
+                                           const GradMaps &maps, unsigned char *sm)
 {
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int n;
-    LatentSpan sp;
-    long long r0;
-    if (!latent_slot(DQ ? a.cu_q : a.cu_k, a, DQ ? a.T : a.Tk, !DQ, TL, slot, &n, &sp, &r0)) return;   // uniform
     const long long Lq = sp.q1 - sp.q0, Lk = sp.k1 - sp.k0, shift = Lk - Lq;
     const long long row_first = (DQ ? sp.q0 : sp.k0) + r0, rows = (DQ ? Lq : Lk) - r0;     // rows: may exceed the tile
     const long long col_first = DQ ? sp.k0 : sp.q0, cols = DQ ? Lk : Lq;
@@ -382,15 +378,11 @@ enum { V_RES, V_QF, V_QE = V_QF + NVQ, V_DF = V_QE + NVQ, V_DE = V_DF + 2, V_S =
        V_DRAIN = V_PV + 2, V_NBARS };
 constexpr uint32_t TV_S = 0, TV_O = 256;
 
-__device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArgs &b, long long slot, int h, const GradMaps &maps,
-                                         unsigned char *sm)
+__device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArgs &b, const LatentSpan &sp, long long r0, int h,
+                                         const GradMaps &maps, unsigned char *sm)
 {
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int n;
-    LatentSpan sp;
-    long long r0;
-    if (!latent_slot(a.cu_k, a, a.Tk, true, 2 * TL, slot, &n, &sp, &r0)) return;   // uniform
     const long long Lq = sp.q1 - sp.q0, Lk = sp.k1 - sp.k0, shift = Lk - Lq, rows = Lk - r0;
     const long long row_first = sp.k0 + r0;
     // query tiles that see some key of tile i: from the first that sees its first key to the last
@@ -622,11 +614,12 @@ __device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArg
     if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
-// One launch for the three: blocks of dq, then of dk, then of dv, each kind from its longest row of tiles to its
-// shortest, so that a kind's last blocks do not leave the GPU idle.
+// One launch for the three: blocks of dq, then of dk, then of dv, so that a kind's last blocks do not leave the GPU
+// idle, each kind from a sequence's longest row of tiles to its shortest. (Ranking the tiles of all sequences, as the
+// forward kernel does, cost these shorter blocks more than it gave: 105 us became 120, 6 sequences x 8 heads.)
 __global__ void __launch_bounds__(NT, 1)
-latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_slots, const __grid_constant__ GradMaps mq,
-                  const __grid_constant__ GradMaps mk)
+latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_slots, long long v_slots,
+                  const __grid_constant__ GradMaps mq, const __grid_constant__ GradMaps mk)
 {
     extern __shared__ __align__(1024) unsigned char sm[];
     if (blockIdx.x == 0) {
@@ -635,10 +628,20 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
     }
     if (smem_u32(sm) & 1023u) { if (threadIdx.x == 0) set_status(a.status, KDA_ERR_CUDA); return; }   // swizzled tiles need it (it holds)
     const int h = blockIdx.x % a.H;
-    const long long x = blockIdx.x / a.H;
-    if (x < q_slots) grad_block<true>(a, b, q_slots - 1 - x, h, mq, sm);
-    else if (x < q_slots + k_slots) grad_block<false>(a, b, x - q_slots, h, mk, sm);
-    else dv_block(a, b, x - q_slots - k_slots, h, mk, sm);
+    long long x = blockIdx.x / a.H;
+    int kind = 0;                              // dq, dk, dv
+    if (x >= q_slots) { x -= q_slots; kind = 1; }
+    if (kind == 1 && x >= k_slots) { x -= k_slots; kind = 2; }
+    const bool keys = kind > 0;
+    const int tile = kind == 2 ? 2 * TL : TL;
+    const long long slots = kind == 0 ? q_slots : kind == 1 ? k_slots : v_slots;
+    LatentSpan sp;
+    long long r0;
+    int n;
+    if (!latent_slot(keys ? a.cu_k : a.cu_q, a, keys ? a.Tk : a.T, keys, tile, keys ? x : slots - 1 - x, &n, &sp, &r0)) return;
+    if (kind == 0) grad_block<true>(a, b, sp, r0, h, mq, sm);
+    else if (kind == 1) grad_block<false>(a, b, sp, r0, h, mk, sm);
+    else dv_block(a, b, sp, r0, h, mk, sm);
 }
 
 // dr[key] = sum over heads of dr_head[key][h], in fp32 and in head order. 16 keys per block: 16 threads of a
@@ -685,7 +688,7 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
     const GradMaps mq = {q, q, d, k, r, v}, mk = {k, r, v, q, q, d};
     if (tokens > 0)
         latent_stat_kernel<<<(unsigned)(((tokens + 31) / 32 * a.H + 7) / 8), 256, 0, stream>>>(a.out, b.dout, a.lse, b.stat, tokens, a.H);
-    latent_bwd_kernel<<<(unsigned)((q_slots + k_slots + v_slots) * a.H), NT, smem, stream>>>(a, b, q_slots, k_slots, mq, mk);
+    latent_bwd_kernel<<<(unsigned)((q_slots + k_slots + v_slots) * a.H), NT, smem, stream>>>(a, b, q_slots, k_slots, v_slots, mq, mk);
     if (a.R && keys > 0) latent_dr_kernel<<<(unsigned)((keys + 15) / 16), 256, 0, stream>>>(b.dr_head, b.dr, keys, a.H);
     return cudaGetLastError();
 }

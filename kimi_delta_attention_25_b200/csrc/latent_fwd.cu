@@ -48,15 +48,19 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % a.H;
-    const long long slot = slots - 1 - blockIdx.x / a.H;
     if (blockIdx.x == 0) {
         check_offsets(a.cu_q, a.N, a.T, a.status);
         check_offsets(a.cu_k, a.N, a.Tk, a.status);
     }
-    int n;
     LatentSpan span;
     long long r0;                              // the block's first row within its sequence
-    if (!latent_slot(a.cu_q, a, a.T, false, 2 * QT, slot, &n, &span, &r0)) return;   // uniform
+    if (a.N > 1 && slots <= kRankedSlots) {
+        if (!latent_ranked(a, 2 * QT, (int)slots, (int)(blockIdx.x / a.H), reinterpret_cast<int *>(sm), &span, &r0)) return;
+        fence_proxy_async_smem();
+    } else {
+        int n;
+        if (!latent_slot(a.cu_q, a, a.T, false, 2 * QT, slots - 1 - blockIdx.x / a.H, &n, &span, &r0)) return;   // uniform
+    }
     struct { long long q0, qn, k0, kn; } t = {span.q0 + r0, span.q1 - span.q0 - r0, span.k0, span.k1 - span.k0};
     // tiles of keys that some row of query tile i sees: row r of the sequence sees keys up to r + Lk - Lq
     const long long shift = t.kn - (span.q1 - span.q0);
