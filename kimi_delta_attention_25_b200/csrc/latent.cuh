@@ -36,7 +36,7 @@ __device__ __forceinline__ bool latent_span(const int32_t *cu_q, const int32_t *
 // The sequence that holds token `tok` of offsets `cu` (or of B rows of T tokens), by bisection; -1 if none does.
 __device__ __forceinline__ int latent_sequence(const int32_t *cu, int N, int T, long long tok)
 {
-    if (!cu) return (int)(tok / T);
+    if (!cu) return (int)((uint32_t)tok / (uint32_t)T);       // B T tokens are below 2^31
     int lo = 0, hi = N - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;

@@ -27,40 +27,90 @@ constexpr int NT = 8 * 32 + 96, W_LOAD = 8, W_MMA = 9;   // two issuing warps (o
 constexpr uint32_t UNIT = 16384;              // 128 rows x 64 channels, 128-byte swizzle
 constexpr uint32_t SMEM_MAX = 232448;
 
-// lse in the log2 domain and D_i = do_i . o_i as [H][tokens] (the dk and dv blocks read them along the
-// tokens): one warp per head and 32 tokens, half a warp to a row.
-__global__ void __launch_bounds__(256) latent_stat_kernel(const __nv_bfloat16 *__restrict__ out, const __nv_bfloat16 *__restrict__ dout,
-                                                          const float *__restrict__ lse, float *__restrict__ stat, long long tokens, int H)
+// Eight bf16 products added up.
+__device__ __forceinline__ float dot8(const uint4 &x, const uint4 &y)
 {
-    const long long warp = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31, h = (int)(warp % H);
-    const long long t0 = warp / H * 32;
-    if (t0 >= tokens) return;
-    float mine = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < 16; ++i) {
-        const long long t = t0 + 2 * i + (lane >> 4);
-        float s = 0.f;
-        if (t < tokens) {
-            const uint4 o = reinterpret_cast<const uint4 *>(out + (t * H + h) * kHeadDim)[lane & 15];
-            const uint4 d = reinterpret_cast<const uint4 *>(dout + (t * H + h) * kHeadDim)[lane & 15];
-            const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, dw[4] = {d.x, d.y, d.z, d.w};
+    const uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+    float s = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s += __uint_as_float(ow[e] << 16) * __uint_as_float(dw[e] << 16);
-                s += __uint_as_float(ow[e] & 0xFFFF0000u) * __uint_as_float(dw[e] & 0xFFFF0000u);
+    for (int e = 0; e < 4; ++e) {
+        s += __uint_as_float(a[e] << 16) * __uint_as_float(b[e] << 16);
+        s += __uint_as_float(a[e] & 0xFFFF0000u) * __uint_as_float(b[e] & 0xFFFF0000u);
+    }
+    return s;
+}
+
+// lse in the log2 domain and D_i = do_i . o_i as [H][tokens] (the dk and dv blocks read them along the
+// tokens): one warp per head and two tokens, half a warp to a row.
+// `out` has been rounded to bf16, which moves D by up to 2^-8 of |do| . |o|. Beside the rounding of dS itself that
+// matters where a row sees few keys (dS is then a difference of nearly equal values, and o as large as v): rows
+// that see at most kShortRow keys get D = sum_j P_ij dP_ij instead, from the same sums in fp32.
+constexpr int kShortRow = 16;
+__global__ void __launch_bounds__(256) latent_stat_kernel(LatentArgs a, const __nv_bfloat16 *__restrict__ dout, float *__restrict__ stat,
+                                                          long long tokens)
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int H = a.H, lane = threadIdx.x & 31, h = blockIdx.y;
+    const long long t0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 2, tok = t0 + (lane >> 4);
+    if (t0 >= tokens) return;
+    const bool real = tok < tokens;
+    uint4 o = make_uint4(0, 0, 0, 0), od = o;
+    float l = 0.f;
+    if (real) {
+        o = reinterpret_cast<const uint4 *>(a.out + (tok * H + h) * kHeadDim)[lane & 15];
+        od = reinterpret_cast<const uint4 *>(dout + (tok * H + h) * kHeadDim)[lane & 15];
+        l = a.lse[tok * H + h];
+    }
+    long long k0 = 0, seen = 0;                // the keys that this half warp's token sees
+    if (real) {
+        const int n = latent_sequence(a.cu_q, a.N, a.T, tok);
+        LatentSpan s;
+        if (n >= 0 && latent_span(a.cu_q, a.cu_k, n, a.T, a.Tk, &s)) {
+            k0 = s.k0;
+            seen = s.k1 - s.k0;
+            if (a.causal) seen = min(seen, tok - s.q0 + (s.k1 - s.k0) - (s.q1 - s.q0) + 1);
+        }
+    }
+    float mine = dot8(o, od);
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, m);
+    for (uint32_t todo = __ballot_sync(0xffffffffu, (lane & 15) == 0 && seen > 1 && seen <= kShortRow); todo; todo &= todo - 1) {
+        // eight lanes to a key, four keys at a time, every load of the row on its way at once
+        const int i = __ffs(todo) - 1, W = kHeadDim + a.R, part = lane & 7;
+        const long long t = t0 + (i >> 4), first = __shfl_sync(0xffffffffu, k0, i);
+        const int cnt = (int)__shfl_sync(0xffffffffu, seen, i);
+        const float li = __shfl_sync(0xffffffffu, l, i);
+        const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (t * H + h) * W), *d = reinterpret_cast<const uint4 *>(dout + (t * H + h) * kHeadDim);
+        const uint4 q0 = q[part], q1 = q[8 + part], q2 = a.R ? q[16 + part] : make_uint4(0, 0, 0, 0), d0 = d[part], d1 = d[8 + part];
+        float x[kShortRow / 4], dp[kShortRow / 4], sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < kShortRow / 4; ++u) {
+            const int j = 4 * u + (lane >> 3);
+            x[u] = dp[u] = 0.f;
+            if (j < cnt) {
+                const uint4 *k = reinterpret_cast<const uint4 *>(a.k + (first + j) * a.k_tok + h * a.k_head);
+                const uint4 *v = reinterpret_cast<const uint4 *>(a.v + (first + j) * a.v_tok + h * a.v_head);
+                x[u] = dot8(q0, k[part]) + dot8(q1, k[8 + part]);
+                if (a.R) x[u] += dot8(q2, reinterpret_cast<const uint4 *>(a.r + (first + j) * a.r_tok)[part]);
+                dp[u] = dot8(d0, v[part]) + dot8(d1, v[8 + part]);
             }
         }
 #pragma unroll
-        for (int m = 8; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-        const float even = __shfl_sync(0xffffffffu, s, 0), odd = __shfl_sync(0xffffffffu, s, 16);
-        if (lane == 2 * i) mine = even;
-        if (lane == 2 * i + 1) mine = odd;
+        for (int u = 0; u < kShortRow / 4; ++u) {
+#pragma unroll
+            for (int m = 4; m > 0; m >>= 1) {
+                x[u] += __shfl_xor_sync(0xffffffffu, x[u], m);
+                dp[u] += __shfl_xor_sync(0xffffffffu, dp[u], m);
+            }
+            if (4 * u + (lane >> 3) < cnt) sum += expf(x[u] * a.scale - li) * dp[u];
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (lane == i) mine = sum;
     }
-    if (t0 + lane < tokens) {
-        const float l = lse[(t0 + lane) * H + h];
-        stat[h * tokens + t0 + lane] = l == -INFINITY ? INFINITY : l * 1.44269504088896341f;
-        stat[tokens * H + h * tokens + t0 + lane] = mine;
+    if (real && (lane & 15) == 0) {
+        stat[(long long)h * tokens + tok] = l == -INFINITY ? INFINITY : l * 1.44269504088896341f;
+        stat[tokens * H + (long long)h * tokens + tok] = mine;
     }
 }
 
@@ -242,13 +292,18 @@ __device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdA
         const float sc = a.scale * 1.44269504088896341f;
         const long long tokens = (long long)a.B * a.T;
         const float *st_lse = b.stat + (size_t)h * tokens, *st_d = st_lse + (size_t)tokens * a.H;
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // the statistics' kernel, whose end this block may overlap
         float lse_r = 0.f, d_r = 0.f;                        // dq: this row's
         if (DQ && real) { lse_r = st_lse[row_first + row]; d_r = st_d[row_first + row]; }
         // columns this row meets: [lo, hi) of the sequence
+        // (a query that sees one key has P = 1 whatever its score: dS is 0, which dP - D would miss by a rounding)
         long long lo = 0, hi = real ? cols : 0;
-        if (a.causal) {
-            if (DQ) hi = min(hi, r0 + row + shift + 1);
-            else lo = r0 + row - shift;
+        if (DQ) {
+            if (a.causal) hi = min(hi, r0 + row + shift + 1);
+            if (hi == 1) hi = 0;
+        } else {
+            if (a.causal) lo = r0 + row > 0 ? r0 + row - shift : 1 - shift;
+            if (Lk == 1) hi = 0;
         }
         const int lo_w = __reduce_max_sync(0xffffffffu, (int)max(lo, 0LL)), hi_w = __reduce_min_sync(0xffffffffu, (int)max(hi, 0LL));
         float *stat = reinterpret_cast<float *>(sm + G_STAT);
@@ -526,6 +581,7 @@ __device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArg
         const bool real = row < rows;
         const float sc = a.scale * 1.44269504088896341f;
         const float *st_lse = b.stat + (size_t)h * ((long long)a.B * a.T);
+        asm volatile("griddepcontrol.wait;" ::: "memory");          // the statistics' kernel
         const long long lo = a.causal ? r0 + row - shift : 0;       // first query that sees this key
         const int lo_w = __reduce_max_sync(0xffffffffu, (int)max(lo, 0LL));
         float *stat = reinterpret_cast<float *>(sm + V_STAT) + i * TL;
@@ -626,7 +682,6 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
         check_offsets(a.cu_q, a.N, a.T, a.status);
         check_offsets(a.cu_k, a.N, a.Tk, a.status);
     }
-    if (smem_u32(sm) & 1023u) { if (threadIdx.x == 0) set_status(a.status, KDA_ERR_CUDA); return; }   // swizzled tiles need it (it holds)
     const int h = blockIdx.x % a.H;
     long long x = blockIdx.x / a.H;
     int kind = 0;                              // dq, dk, dv
@@ -638,7 +693,16 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
     LatentSpan sp;
     long long r0;
     int n;
-    if (!latent_slot(keys ? a.cu_k : a.cu_q, a, keys ? a.Tk : a.T, keys, tile, keys ? x : slots - 1 - x, &n, &sp, &r0)) return;
+    bool some = latent_slot(keys ? a.cu_k : a.cu_q, a, keys ? a.Tk : a.T, keys, tile, keys ? x : slots - 1 - x, &n, &sp, &r0);
+    if (smem_u32(sm) & 1023u) {                // swizzled tiles need it (it holds)
+        if (threadIdx.x == 0) set_status(a.status, KDA_ERR_CUDA);
+        some = false;
+    }
+    if (!some) {
+        // no block ends before the statistics' kernel has: what follows this kernel must not overtake that one
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     if (kind == 0) grad_block<true>(a, b, sp, r0, h, mq, sm);
     else if (kind == 1) grad_block<false>(a, b, sp, r0, h, mk, sm);
     else dv_block(a, b, sp, r0, h, mk, sm);
@@ -687,8 +751,20 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
     if (e != cudaSuccess) return e;
     const GradMaps mq = {q, q, d, k, r, v}, mk = {k, r, v, q, q, d};
     if (tokens > 0)
-        latent_stat_kernel<<<(unsigned)(((tokens + 31) / 32 * a.H + 7) / 8), 256, 0, stream>>>(a.out, b.dout, a.lse, b.stat, tokens, a.H);
-    latent_bwd_kernel<<<(unsigned)((q_slots + k_slots + v_slots) * a.H), NT, smem, stream>>>(a, b, q_slots, k_slots, v_slots, mq, mk);
+        latent_stat_kernel<<<dim3((unsigned)((tokens + 15) / 16), a.H), 256, 0, stream>>>(a, b.dout, b.stat, tokens);
+    // its blocks set up and load their first tiles while the statistics are being finished
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((q_slots + k_slots + v_slots) * a.H));
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &at;
+    cfg.numAttrs = tokens > 0 ? 1 : 0;
+    const cudaError_t e2 = cudaLaunchKernelEx(&cfg, latent_bwd_kernel, a, b, q_slots, k_slots, v_slots, mq, mk);
+    if (e2 != cudaSuccess) return e2;
     if (a.R && keys > 0) latent_dr_kernel<<<(unsigned)((keys + 15) / 16), 256, 0, stream>>>(b.dr_head, b.dr, keys, a.H);
     return cudaGetLastError();
 }

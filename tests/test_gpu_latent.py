@@ -203,6 +203,27 @@ def test_expanded_empty_sizes():
     assert all(torch.all(g[x] == 0) for x in ("dk", "dv", "dk_shared"))
 
 
+def test_expanded_gradients_of_short_rows():
+    """Rows that see one key have no gradient through the softmax (exactly), and those that see a few keep their
+    accuracy although ``out`` was rounded: over all rows two roundings to bf16, each at most 2^-8 of a value and of
+    2^-8 / sqrt(3) in the mean square, stay below 2^-8 of the gradients' 2-norm."""
+    for lens_q, lens_k in (([1] * 16, [1] * 16), ([1, 2, 1, 3, 2, 4, 5, 2, 9, 17, 3, 2], [1, 2, 1, 3, 2, 4, 5, 2, 9, 17, 3, 2]),
+                           ([3, 40, 5], [1, 2, 4]), ([2, 200], [3, 201])):
+        for causal in (True, False):
+            q, k, v, r, dout = expanded(lens_q, lens_k, 3, 64, seed=21)
+            cu = (cu_of(lens_q), cu_of(lens_k))
+            out, lse = kda.latent_fwd(q, k, v, r, *cu, causal=causal)
+            g = kda.latent_bwd(q, k, v, r, out, lse, dout, *cu, causal=causal)
+            ref = O.backward(f64(q)[0], f64(k)[0], f64(v)[0], f64(r)[0], f64(dout)[0], cu[0].cpu().numpy(), cu[1].cpu().numpy(),
+                             float(np.float32(192 ** -0.5)), causal)
+            for key, name in (("dq", "dq"), ("dk", "dk"), ("dv", "dv"), ("dk_shared", "dr")):
+                off, size = np.linalg.norm(f64(g[key])[0] - ref[name]), np.linalg.norm(ref[name])
+                if size < 1e-12:
+                    assert off == 0, (key, lens_q, causal)
+                else:
+                    assert off <= 2.0 ** -8 * size, (key, lens_q, causal, off / size)
+
+
 def test_expanded_gradients_against_differences():
     """The directional derivative of the forward itself, taken by central differences in its inputs."""
     lens = [90, 45]
