@@ -152,16 +152,7 @@ __device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdA
     const int nt = t_hi - t_lo;
 
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G_BAR);
-    volatile int *ctl = reinterpret_cast<volatile int *>(bars + G_NBARS);      // [0] tensor memory, [1] abort
-    if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
-    if (tid == 0) {
-        for (int i = 0; i < G_NBARS; ++i) mbar_init(&bars[i], (i == G_SFREE || i == G_PFREE || i == G_DS) ? 8 : 1);
-        ctl[1] = 0;
-        fence_mbar_init();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    volatile int *ctl = reinterpret_cast<volatile int *>(bars + G_NBARS);
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
     volatile int *abort_flag = ctl + 1;
     auto wait = [&](int x, uint32_t parity) {
@@ -398,39 +389,39 @@ __device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdA
             __syncwarp();
             tc_fence_after();
         }
-        // results: chunks of 16 columns, the two warpgroups in turn
+        // results: chunks of 32 columns, the two warpgroups in turn
         const size_t at = (size_t)(row_first + row) * a.H + h;
 #pragma unroll 1
-        for (int c = g * 16; c < u1 * 64; c += 32) {
-            float o[16];
-            if (nt > 0) tmem_ld16_sync(tmem + TM_ACC + lanes + c, o);
+        for (int c = g * 32; c < u1 * 64; c += 64) {
+            float o[32];
+            if (nt > 0) tmem_ld32_sync(tmem + TM_ACC + lanes + c, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = nt > 0 ? o[e] * a.scale : 0.f;
+            for (int e = 0; e < 32; ++e) o[e] = nt > 0 ? o[e] * a.scale : 0.f;
             if (!real) continue;
             if (!DQ && c >= kHeadDim) {
                 float4 *dst = reinterpret_cast<float4 *>(b.dr_head + at * kSharedDim + c - kHeadDim);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             } else {
                 uint4 *dst = reinterpret_cast<uint4 *>(DQ ? b.dq + at * (kHeadDim + a.R) + c : b.dk + at * kHeadDim + c);
-                dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-                dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]), pack_bf16x2(o[14], o[15]));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                        pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
             }
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------------------------------ dv
 // The forward kernel's structure with the roles of queries and keys exchanged and lse known: two key tiles at
 // once, P^T over S^T's columns as the A operand of dv += P^T dO.
 constexpr int NVQ = 4;                        // ring of query units; dO has two tiles
-constexpr uint32_t V_A = 0, V_Q = 6 * UNIT, V_D = V_Q + NVQ * UNIT, V_STAT = V_D + 4 * UNIT, V_BAR = V_STAT + 1024, V_END = V_BAR + 320;
-static_assert(V_END <= SMEM_MAX, "shared memory");
+constexpr uint32_t V_A = 0, V_Q = 6 * UNIT, V_D = V_Q + NVQ * UNIT, V_STAT = V_D + 4 * UNIT, V_BAR = G_BAR;
+static_assert(V_STAT + 1024 <= V_BAR, "shared memory");
 enum { V_RES, V_QF, V_QE = V_QF + NVQ, V_DF = V_QE + NVQ, V_DE = V_DF + 2, V_S = V_DE + 2, V_PA = V_S + 2, V_PB = V_PA + 2, V_PV = V_PB + 2,
        V_DRAIN = V_PV + 2, V_NBARS };
+static_assert(V_NBARS <= G_NBARS, "barriers");
 constexpr uint32_t TV_S = 0, TV_O = 256;
 
 __device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArgs &b, const LatentSpan &sp, long long r0, int h,
@@ -452,16 +443,7 @@ __device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArg
     const int nt = t_hi - t_lo;
 
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + V_BAR);
-    volatile int *ctl = reinterpret_cast<volatile int *>(bars + V_NBARS);
-    if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
-    if (tid == 0) {
-        for (int i = 0; i < V_NBARS; ++i) mbar_init(&bars[i], (i >= V_PA && i < V_PV) ? 4 : 1);
-        ctl[1] = 0;
-        fence_mbar_init();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    volatile int *ctl = reinterpret_cast<volatile int *>(bars + G_NBARS);
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
     volatile int *abort_flag = ctl + 1;
     auto wait = [&](int x, uint32_t parity) {
@@ -652,22 +634,19 @@ __device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArg
         }
         const size_t at = (size_t)(row_first + row) * a.H + h;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 16) {
-            float o[16];
-            if (cnt > 0) tmem_ld16_sync(to + c, o);
-            uint32_t w[8];
+        for (int c = 0; c < 128; c += 32) {
+            float o[32];
+            if (cnt > 0) tmem_ld32_sync(to + c, o);
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = cnt > 0 ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : 0u;
+            for (int e = 0; e < 16; ++e) w[e] = cnt > 0 ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : 0u;
             if (real) {
                 uint4 *dst = reinterpret_cast<uint4 *>(b.dv + at * kHeadDim + c);
-                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
             }
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
 // One launch for the three: blocks of dq, then of dk, then of dv, so that a kind's last blocks do not leave the GPU
@@ -682,12 +661,26 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
         check_offsets(a.cu_q, a.N, a.T, a.status);
         check_offsets(a.cu_k, a.N, a.Tk, a.status);
     }
-    const int h = blockIdx.x % a.H;
+    const int h = blockIdx.x % a.H, warp = threadIdx.x >> 5;
     long long x = blockIdx.x / a.H;
     int kind = 0;                              // dq, dk, dv
     if (x >= q_slots) { x -= q_slots; kind = 1; }
     if (kind == 1 && x >= k_slots) { x -= k_slots; kind = 2; }
     const bool keys = kind > 0;
+    // tensor memory and barriers, beside the search for the block's tile
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G_BAR);
+    volatile int *ctl = reinterpret_cast<volatile int *>(bars + G_NBARS);      // [0] tensor memory, [1] abort
+    if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
+    if (warp == W_LOAD && elect_one()) {
+        for (int i = 0; i < (kind == 2 ? V_NBARS : G_NBARS); ++i) {
+            const bool by_warps = kind == 2 ? i >= V_PA && i < V_PV : i == G_SFREE || i == G_PFREE || i == G_DS;
+            mbar_init(&bars[i], by_warps ? (kind == 2 ? 4 : 8) : 1);
+        }
+        ctl[1] = 0;
+        fence_mbar_init();
+        const GradMaps &m = kind == 0 ? mq : mk;
+        if (a.T > 0 && a.Tk > 0) { tma_prefetch_desc(&m.a1); tma_prefetch_desc(&m.a2); tma_prefetch_desc(&m.b1); tma_prefetch_desc(&m.b2); }
+    }
     const int tile = kind == 2 ? 2 * TL : TL;
     const long long slots = kind == 0 ? q_slots : kind == 1 ? k_slots : v_slots;
     LatentSpan sp;
@@ -698,14 +691,23 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
         if (threadIdx.x == 0) set_status(a.status, KDA_ERR_CUDA);
         some = false;
     }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
     if (!some) {
         // no block ends before the statistics' kernel has: what follows this kernel must not overtake that one
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
+    } else if (kind == 0) {
+        grad_block<true>(a, b, sp, r0, h, mq, sm);
+    } else if (kind == 1) {
+        grad_block<false>(a, b, sp, r0, h, mk, sm);
+    } else {
+        dv_block(a, b, sp, r0, h, mk, sm);
     }
-    if (kind == 0) grad_block<true>(a, b, sp, r0, h, mq, sm);
-    else if (kind == 1) grad_block<false>(a, b, sp, r0, h, mk, sm);
-    else dv_block(a, b, sp, r0, h, mk, sm);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
 // dr[key] = sum over heads of dr_head[key][h], in fp32 and in head order. 16 keys per block: 16 threads of a
@@ -746,7 +748,7 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
                      !bf16_heads_map(&v, a.v, kHeadDim, a.H, keys, a.v_head, a.v_tok, 64, TL) ||
                      (a.R && !bf16_rows_map(&r, a.r, kSharedDim, keys, a.r_tok, 64, TL))))
         return cudaErrorNotSupported;
-    constexpr uint32_t smem = G_END > V_END ? G_END : V_END;
+    constexpr uint32_t smem = G_END;
     const cudaError_t e = cudaFuncSetAttribute(latent_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const GradMaps mq = {q, q, d, k, r, v}, mk = {k, r, v, q, q, d};

@@ -52,28 +52,7 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
         check_offsets(a.cu_q, a.N, a.T, a.status);
         check_offsets(a.cu_k, a.N, a.Tk, a.status);
     }
-    LatentSpan span;
-    long long r0;                              // the block's first row within its sequence
-    if (a.N > 1 && slots <= kRankedSlots) {
-        if (!latent_ranked(a, 2 * QT, (int)slots, (int)(blockIdx.x / a.H), reinterpret_cast<int *>(sm), &span, &r0)) return;
-        fence_proxy_async_smem();
-    } else {
-        int n;
-        if (!latent_slot(a.cu_q, a, a.T, false, 2 * QT, slots - 1 - blockIdx.x / a.H, &n, &span, &r0)) return;   // uniform
-    }
-    struct { long long q0, qn, k0, kn; } t = {span.q0 + r0, span.q1 - span.q0 - r0, span.k0, span.k1 - span.k0};
-    // tiles of keys that some row of query tile i sees: row r of the sequence sees keys up to r + Lk - Lq
-    const long long shift = t.kn - (span.q1 - span.q0);
-    int nt[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const long long last = min(r0 + (i + 1) * QT, span.q1 - span.q0) - 1;      // the tile's last row
-        long long keys = a.causal ? min(t.kn, last + shift + 1) : t.kn;
-        if (i * QT >= t.qn || keys < 0) keys = 0;
-        nt[i] = (int)((keys + KT - 1) / KT);
-    }
-    const int ntile = max(nt[0], nt[1]);
-
+    // tensor memory and barriers, beside the search for the block's tile
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
     volatile int *ctl = reinterpret_cast<volatile int *>(bars + N_BARS);      // [0] tensor memory, [1] abort
     if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
@@ -91,11 +70,39 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
         mbar_init(&bars[B_DRAIN], 1);
         ctl[1] = 0;
         fence_mbar_init();
+        if (a.Tk > 0) { tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v); }
+    }
+    LatentSpan span;
+    long long r0;                              // the block's first row within its sequence
+    bool some;
+    if (a.N > 1 && slots <= kRankedSlots) {
+        some = latent_ranked(a, 2 * QT, (int)slots, (int)(blockIdx.x / a.H), reinterpret_cast<int *>(sm), &span, &r0);
+        fence_proxy_async_smem();
+    } else {
+        int n;
+        some = latent_slot(a.cu_q, a, a.T, false, 2 * QT, slots - 1 - blockIdx.x / a.H, &n, &span, &r0);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
+    if (!some) {                               // uniform
+        if (warp == W_MMA) tmem_dealloc(tmem, 512);
+        return;
+    }
+    struct { long long q0, qn, k0, kn; } t = {span.q0 + r0, span.q1 - span.q0 - r0, span.k0, span.k1 - span.k0};
+    // tiles of keys that some row of query tile i sees: row r of the sequence sees keys up to r + Lk - Lq
+    const long long shift = t.kn - (span.q1 - span.q0);
+    int nt[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const long long last = min(r0 + (i + 1) * QT, span.q1 - span.q0) - 1;      // the tile's last row
+        long long keys = a.causal ? min(t.kn, last + shift + 1) : t.kn;
+        if (i * QT >= t.qn || keys < 0) keys = 0;
+        nt[i] = (int)((keys + KT - 1) / KT);
+    }
+    const int ntile = max(nt[0], nt[1]);
+
     volatile int *abort_flag = ctl + 1;
     auto wait = [&](int b, uint32_t parity) {
         if (mbar_try_wait(&bars[b], parity)) return true;
@@ -111,7 +118,6 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
     if (warp == W_LOAD) {
         // ============================================================================ loader
         if (elect_one() && ntile > 0) {
-            tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v);
             mbar_arrive_expect_tx(&bars[B_Q], 2 * kunits * UNIT);
             for (int i = 0; i < 2; ++i)
                 for (int u = 0; u < kunits; ++u)
@@ -318,16 +324,16 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
         const size_t orow = (size_t)(t.q0 + row) * a.H + h;
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 16) {
-            float o[16];
-            if (nti > 0) tmem_ld16_sync(to + c, o);
-            uint32_t w[8];
+        for (int c = 0; c < 128; c += 32) {
+            float o[32];
+            if (nti > 0) tmem_ld32_sync(to + c, o);
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = nti > 0 ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
+            for (int e = 0; e < 16; ++e) w[e] = nti > 0 ? pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv) : 0u;
             if (real) {
                 uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + c);
-                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
             }
         }
         if (real) a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;

@@ -101,7 +101,7 @@ def _expanded(q, k, v, k_shared, cu_q, cu_k):
 
 def _workspace(workspace, size, like):
     if workspace is None:
-        return torch.empty(max(size, 256), dtype=torch.uint8, device=like.device)
+        return like.new_empty((max(size, 256),), dtype=torch.uint8)
     _check("workspace", workspace, torch.uint8, like.get_device())
     return workspace
 
@@ -266,7 +266,7 @@ def rms_norm_e4m3(x, weight, residual=None, eps=1e-5, out=None, scale=None, resi
     else:
         _check("out", out, torch.float8_e4m3fn, dev, x.shape)
     if scale is None:
-        scale = x.new_empty((*x.shape[:-1], D // 128), dtype=_F32)
+        scale = weight.new_empty((*x.shape[:-1], D // 128))
     else:
         _check("scale", scale, _F32, dev, (*x.shape[:-1], D // 128))
     _call("kda_rms_norm_e4m3", dev, (_p(x), _p(residual), _p(weight), _p(out), _p(scale), _p(h),
@@ -295,7 +295,7 @@ def rms_norm_bwd(dy, h, weight, dh=None, eps=1e-5, dx=None, dweight=None, worksp
     else:
         _check("dx", dx, h.dtype, dev, h.shape)
     if dweight is None:
-        dweight = h.new_empty((D,), dtype=_F32)
+        dweight = torch.empty_like(weight)
     else:
         _check("dweight", dweight, _F32, dev, (D,))
     rows = h.numel() // D if D else 0
