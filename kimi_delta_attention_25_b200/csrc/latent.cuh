@@ -121,6 +121,15 @@ __device__ __forceinline__ void check_offsets(const int32_t *cu, int N, int T, i
     }
 }
 
+// Clears the status word and checks both offset arrays: the first block of a call's first kernel, all its threads.
+__device__ __forceinline__ void check_call(const LatentArgs &a)
+{
+    if (threadIdx.x == 0) *a.status = KDA_OK;
+    __syncthreads();
+    check_offsets(a.cu_q, a.N, a.T, a.status);
+    check_offsets(a.cu_k, a.N, a.Tk, a.status);
+}
+
 // Host checks of the expanded form's arguments, and the description they give.
 kda_status_t check_latent(const void *q, const void *k, const void *v, const void *k_shared, const int32_t *cu_q,
                           const int32_t *cu_k, const void *out, const float *lse, int B, int T, int Tk, int H, int N,

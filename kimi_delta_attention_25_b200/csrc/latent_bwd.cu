@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(256) latent_stat_kernel(LatentArgs a, const __
                                                           long long tokens)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_call(a);
     const int H = a.H, lane = threadIdx.x & 31, h = blockIdx.y;
     const long long t0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 2, tok = t0 + (lane >> 4);
     if (t0 >= tokens) return;
@@ -421,7 +422,7 @@ constexpr uint32_t V_A = 0, V_Q = 6 * UNIT, V_D = V_Q + NVQ * UNIT, V_STAT = V_D
 static_assert(V_STAT + 1024 <= V_BAR, "shared memory");
 enum { V_RES, V_QF, V_QE = V_QF + NVQ, V_DF = V_QE + NVQ, V_DE = V_DF + 2, V_S = V_DE + 2, V_PA = V_S + 2, V_PB = V_PA + 2, V_PV = V_PB + 2,
        V_DRAIN = V_PV + 2, V_NBARS };
-static_assert(V_NBARS <= G_NBARS, "barriers");
+static_assert((int)V_NBARS <= (int)G_NBARS, "barriers");
 constexpr uint32_t TV_S = 0, TV_O = 256;
 
 __device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArgs &b, const LatentSpan &sp, long long r0, int h,
@@ -649,23 +650,21 @@ __device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArg
     }
 }
 
-// One launch for the three: blocks of dq, then of dk, then of dv, so that a kind's last blocks do not leave the GPU
-// idle, each kind from a sequence's longest row of tiles to its shortest. (Ranking the tiles of all sequences, as the
-// forward kernel does, cost these shorter blocks more than it gave: 105 us became 120, 6 sequences x 8 heads.)
+// One launch for the three: blocks of dv, then of dk, then of dq, so that a kind's last blocks do not leave the GPU
+// idle and the longest blocks (dv: two tiles of rows) are not the last, each kind from a sequence's longest row of tiles
+// to its shortest. (Ranking the tiles of all sequences, as the forward kernel does, cost these shorter blocks more than
+// it gave: 105 us became 120, 6 sequences x 8 heads.)
 __global__ void __launch_bounds__(NT, 1)
 latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_slots, long long v_slots,
                   const __grid_constant__ GradMaps mq, const __grid_constant__ GradMaps mk)
 {
     extern __shared__ __align__(1024) unsigned char sm[];
-    if (blockIdx.x == 0) {
-        check_offsets(a.cu_q, a.N, a.T, a.status);
-        check_offsets(a.cu_k, a.N, a.Tk, a.status);
-    }
+    if (blockIdx.x == 0 && a.T == 0) check_call(a);              // (else the statistics' kernel does)
     const int h = blockIdx.x % a.H, warp = threadIdx.x >> 5;
     long long x = blockIdx.x / a.H;
-    int kind = 0;                              // dq, dk, dv
-    if (x >= q_slots) { x -= q_slots; kind = 1; }
-    if (kind == 1 && x >= k_slots) { x -= k_slots; kind = 2; }
+    int kind = 2;                              // 0 dq, 1 dk, 2 dv
+    if (x >= v_slots) { x -= v_slots; kind = 1; }
+    if (kind == 1 && x >= k_slots) { x -= k_slots; kind = 0; }
     const bool keys = kind > 0;
     // tensor memory and barriers, beside the search for the block's tile
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G_BAR);
@@ -737,7 +736,6 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
     const long long tokens = (long long)a.B * a.T, keys = (long long)a.B * a.Tk;
     const long long q_slots = tokens > 0 ? tokens / TL + a.N : 0, k_slots = keys > 0 ? keys / TL + a.N : 0;
     const long long v_slots = keys > 0 ? keys / (2 * TL) + a.N : 0;
-    if (q_slots + k_slots == 0) return cudaSuccess;
     if ((q_slots + k_slots + v_slots) * a.H > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int W = kHeadDim + a.R;
     CUtensorMap q = {}, k = {}, r = {}, v = {}, d = {};          // an empty side's tiles are never copied
@@ -810,8 +808,7 @@ kda_status_t kda_latent_bwd(const void *q, const void *k, const void *v, const v
     b.stat = (float *)((unsigned char *)workspace + kStatusBytes);
     b.dr_head = (float *)((unsigned char *)b.stat + align256((size_t)B * T * H * 8));
     cudaStream_t st = (cudaStream_t)stream;
-    if (cudaMemsetAsync(workspace, 0, kStatusBytes, st) != cudaSuccess) return KDA_ERR_CUDA;
-    if (N == 0 || B == 0) return KDA_OK;
+    if (N == 0 || B == 0 || (T == 0 && Tk == 0)) return cudaMemsetAsync(workspace, 0, kStatusBytes, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     return launch_latent_bwd(a, b, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

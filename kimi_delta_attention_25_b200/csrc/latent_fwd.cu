@@ -48,10 +48,7 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % a.H;
-    if (blockIdx.x == 0) {
-        check_offsets(a.cu_q, a.N, a.T, a.status);
-        check_offsets(a.cu_k, a.N, a.Tk, a.status);
-    }
+    if (blockIdx.x == 0) check_call(a);        // (other blocks set the status a second later at the earliest: a wait that ran out)
     // tensor memory and barriers, beside the search for the block's tile
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
     volatile int *ctl = reinterpret_cast<volatile int *>(bars + N_BARS);      // [0] tensor memory, [1] abort
@@ -420,8 +417,7 @@ kda_status_t kda_latent_fwd(const void *q, const void *k, const void *v, const v
     if (s != KDA_OK) return s;
     a.causal = causal != 0;
     cudaStream_t st = (cudaStream_t)stream;
-    if (cudaMemsetAsync(workspace, 0, kStatusBytes, st) != cudaSuccess) return KDA_ERR_CUDA;
-    if ((long long)B * T == 0 || N == 0) return KDA_OK;
+    if ((long long)B * T == 0 || N == 0) return cudaMemsetAsync(workspace, 0, kStatusBytes, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
     return launch_latent_fwd(a, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
