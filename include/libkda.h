@@ -406,6 +406,8 @@ kda_status_t kda_chunk_fwd_noalloc_status(void *stream, int32_t *status);
  *   out        [B, T, H, 128] bf16 (written)
  *   lse        [B, T, H] float32 (written): log sum_j exp(s_ij)
  *              A query that sees no key gets out = 0 and lse = -infinity.
+ * Infinities and NaN stay within their sequence. Within it, a value that is not finite may also reach
+ * queries that the mask hides it from, of the same 128 (0 times it is NaN there).
  *   workspace  kda_latent_fwd_workspace_size(...) bytes; its status word is cleared by the call.
  * Strides are positive multiples of 8; pointers 16-byte aligned (lse, offsets: 4). At most 65535 heads
  * and 65535 sequences. */
@@ -422,7 +424,8 @@ kda_status_t kda_latent_fwd(const void *q, const void *k, const void *v, const v
 /* Backward pass of kda_latent_fwd: the same arguments, its out and lse, and dout [B, T, H, 128] bf16.
  * Written, dense and bf16 (summed in fp32, rounded once): dq [B, T, H, dk + dr], dk_out and dv_out
  * [B, Tk, H, 128], dk_shared [B, Tk, dr] (the sum over the heads; NULL when dr = 0). Results do not
- * depend on timing: no atomic sums. Workspace: kda_latent_bwd_workspace_size(...) bytes. Keys that no
+ * depend on timing: no atomic sums. A query that sees one key has no gradient through its score
+ * (exactly 0). Workspace: kda_latent_bwd_workspace_size(...) bytes. Keys that no
  * query sees get zero gradients. */
 size_t kda_latent_bwd_workspace_size(int B, int T, int Tk, int H, int N, int dr);
 kda_status_t kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_shared,
@@ -446,12 +449,14 @@ kda_status_t kda_latent_bwd(const void *q, const void *k, const void *v, const v
  *              token t sees the first seq_len - Tq + t + 1 rows.
  *   out        [N, Tq, H, dc] bf16, lse [N, Tq, H] float32 (both written); a token that sees no row
  *              gets out = 0 and lse = -infinity.
- * Rows behind a sequence's length may hold anything, infinities and NaN included. A length outside
+ * Rows behind a sequence's length may hold anything, infinities and NaN included (those below it are
+ * values of the sum, 0 times them where only a later token sees them). A length outside
  * [0, max_pages * page_size] (the sequence is then treated as idle) or a page outside [0, num_pages)
  * (the sequence's outputs are then not usable; no memory outside the cache is read) writes
- * KDA_ERR_INVALID_ARG to the status word. num_pages * page_size and max_pages * page_size stay
- * below 2^31. Workspace: kda_latent_decode_workspace_size(...) bytes (partial results of sequences that
- * several blocks share), not shared by calls that may overlap. */
+ * KDA_ERR_INVALID_ARG to the status word. num_pages * page_size and max_pages * page_size are at
+ * most 2^31 - 2^16, N * (max_pages * page_size / 64 + 1) below 2^31, Tq * H at most 65536, N at
+ * most 65535 (else KDA_ERR_UNSUPPORTED). Workspace: kda_latent_decode_workspace_size(...) bytes (partial
+ * results of sequences that several blocks share), not shared by calls that may overlap. */
 size_t kda_latent_decode_workspace_size(int N, int Tq, int H);
 kda_status_t kda_latent_decode_step(const void *q, const void *cache, const int32_t *page_table,
                                     const int32_t *seq_lens, void *out, float *lse,
