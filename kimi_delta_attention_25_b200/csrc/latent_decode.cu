@@ -13,12 +13,12 @@
 //  - The products are limited by what they read from shared memory (A 128 rows x 16 = 4 KB an instruction at
 //    128 bytes a cycle), which the copies' writes share: S^T with M = 64 reads 3 KB where S = Q C^T with
 //    M = 128 (rows behind the queries unused) reads 6 KB and took 52 cycles an instruction (256 sequences x 32
-//    heads, 1.5 GB: 392 us, then 342 with nothing else changed; 282 now, 5.4 TB/s).
-//  - A thread of the softmax has one cache row and half of the query rows. It goes on with the running maxima
+//    heads, 1.5 GB: 392 us, then 342 with nothing else changed; 267 now, 5.7 TB/s).
+//  - A thread of the softmax has one cache row and 16 of the query rows. It goes on with the running maxima
 //    it has and only checks, in the same barrier that the tile needs anyway, whether a score passed one of
 //    them by more than 2^8 (P stays below 2^8, l is fp32): maxima across threads, and the rescaling of O^T in
 //    tensor memory, are for the few tiles where one did.
-//  - The tiles of all sequences form one list, cut into equal shares, one per SM (`lanes`), whatever the
+//  - The tiles of all sequences form one list, cut into equal shares, one per SM, whatever the
 //    sequences' lengths. A sequence that a cut runs through leaves partial results (unnormalised O, maximum,
 //    sum, fp32), which a second kernel joins in order of the shares: no atomics, the same bits each time.
 //    The groups of one sequence (more than 64 rows) take the same share at the same time on neighbouring
