@@ -2,18 +2,14 @@
 // from the forward's lse:  P = exp(s - lse),  D_i = do_i . o_i,  dP = do v^T,  dS = P (dP - D),
 //   dq = scale dS [k, r],  dk = scale dS^T q[:128],  dr = scale sum_h dS^T q[128:],  dv = P^T do.
 //
-// Three kinds of blocks, each for one row of tiles, none of them adding to memory that another block adds to:
-//   dq: rows of 128 queries, over key tiles:    S = Q [K, R]^T, dP = dO V^T,     dq += dS [K, R]
-//   dk: rows of 128 keys, over query tiles:     S^T = [K, R] Q^T, dP^T = V dO^T, dk += dS^T Q
-//   dv: rows of 2 x 128 keys, over query tiles: S^T, dv += P^T dO
-// (the first two are one template: resident operands A1, A2 and streamed ones B1, B2 swap roles). One block
-// for dk and dv would need S^T, dP^T, dk (192 columns) and dv in tensor memory: 576 of 512 columns; with query
-// tiles of 64, which fit, the products over 64 columns read their 128-row operand from shared memory twice as
-// often and cost as much as computing S^T again. A fused dq would need atomic sums or 2 bytes of dS per pair in
-// memory, read and written: about twice the time of recomputing S and dP.
-// The tensor cores bound it: per 128 x 128 tile and head 804 + 536 + 792 cycles for dq and dk each and
-// 804 + 536 for dv, 5600 in all, where a single pass without the recomputation would take 3460.
-// dS (and P) pass through tensor memory in bf16 as A operands; sums, lse and D are fp32.
+// Two kinds of blocks, each for one row of tiles, none of them adding to memory that another block adds to:
+//   dq:        rows of 128 queries, over key tiles:   S = Q [K, R]^T, dP = dO V^T,     dq += dS [K, R]
+//   dk and dv: rows of 128 keys, over query tiles:    S^T = [K, R] Q^T, dP^T = V dO^T, dk, dr += dS^T Q, dv += P^T dO
+// A fused dq would need atomic sums, or dS through memory (2.1 GB written and read for 8192 tokens x 16 heads, 330 us,
+// where computing S and dP again takes 160).
+// The tensor cores bound it: per 128 x 128 tile and head 804 + 536 + 792 cycles for dq and 804 + 3 x 536 + 280 for dk and
+// dv, 4820 in all, where a single pass without the recomputation would take 3460.
+// dS and P pass through tensor memory in bf16 as A operands; sums, lse and D are fp32.
 #include "latent.cuh"
 #include "sm100.cuh"
 
@@ -115,79 +111,111 @@ __global__ void __launch_bounds__(256) latent_stat_kernel(LatentArgs a, const __
     }
 }
 
-// ------------------------------------------------------------------------------------ dq and dk
-// Shared memory: A1 (3 units), A2 (2), a ring of 7 units for B1 and one of 2 for B2, the statistics of the
-// columns (dk: two tiles of 128 values of each kind).
+// What the blocks share: the tensor maps, the barriers' place, and the wait.
+constexpr uint32_t OFF_BAR = 14 * UNIT + 2048, SMEM = OFF_BAR + 320;
+static_assert(SMEM <= SMEM_MAX, "shared memory");
+constexpr int kMaxBars = 36;
+struct BwdMaps { CUtensorMap q, k, r, v, d; };
+
+__device__ __forceinline__ volatile int *control(unsigned char *sm)          // [0] tensor memory, [1] abort
+{
+    return reinterpret_cast<volatile int *>(reinterpret_cast<uint64_t *>(sm + OFF_BAR) + kMaxBars);
+}
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort_flag) return false;
+        if (clock64() - t0 > 2000000000LL) { *abort_flag = 1; set_status(status, KDA_ERR_TIMEOUT); return false; }
+    }
+    return true;
+}
+
+// Results leave through shared memory: a lane has one row, and 16 bytes of 32 rows at a time is what a store writes worst
+// (a block's end took 8 to 10 thousand cycles). C pieces of 16 bytes a row, rows of the stage one piece further apart.
+template <int C>
+__device__ __forceinline__ void stage_piece(unsigned char *stage, int lane, int piece, uint4 x)
+{
+    *reinterpret_cast<uint4 *>(stage + lane * (C * 16 + 16) + piece * 16) = x;
+}
+template <int C>
+__device__ __forceinline__ void store_stage(const unsigned char *stage, int lane, int rows, void *dst, size_t pitch)
+{
+    __syncwarp();
+#pragma unroll 4
+    for (int i = lane; i < 32 * C; i += 32) {
+        const int r = i / C, c = i % C;
+        if (r < rows)
+            *reinterpret_cast<uint4 *>(static_cast<unsigned char *>(dst) + r * pitch + c * 16) =
+                *reinterpret_cast<const uint4 *>(stage + r * (C * 16 + 16) + c * 16);
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ uint4 pack8(const float *x)
+{
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
+// ------------------------------------------------------------------------------------------ dq
+// The two warpgroups take halves of a result's row: C pieces of 16 bytes each.
+template <int C>
+__device__ __forceinline__ void dq_result(uint32_t acc, bool some, float scale, unsigned char *stage, int lane, int rows, __nv_bfloat16 *dst, size_t pitch)
+{
+#pragma unroll
+    for (int c = 0; c < C / 4; ++c) {
+        float o[32];
+        if (some) tmem_ld32_sync(acc + c * 32, o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = some ? o[e] * scale : 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) stage_piece<C>(stage, lane, c * 4 + e, pack8(o + 8 * e));
+    }
+    store_stage<C>(stage, lane, rows, dst, pitch);
+}
+// Shared memory: Q (3 units) and dO (2) of the block's rows, a ring of 7 units for keys and one of 2 for values.
 constexpr int N1 = 7, N2 = 2;
-constexpr uint32_t G_A1 = 0, G_A2 = 3 * UNIT, G_B1 = 5 * UNIT, G_B2 = G_B1 + N1 * UNIT, G_STAT = G_B2 + N2 * UNIT,
-                   G_BAR = G_STAT + 2048, G_END = G_BAR + 320;
-static_assert(G_END <= SMEM_MAX, "shared memory");
+constexpr uint32_t G_A1 = 0, G_A2 = 3 * UNIT, G_B1 = 5 * UNIT, G_B2 = G_B1 + N1 * UNIT;
 enum { G_RES, G_F1, G_E1 = G_F1 + N1, G_F2 = G_E1 + N1, G_E2 = G_F2 + N2, G_S = G_E2 + N2, G_SFREE, G_P, G_PFREE, G_DS,
        G_ACC, G_DRAIN, G_NBARS = G_DRAIN + 2 };
-static_assert(G_NBARS * 8 + 16 <= 320, "barriers");
+static_assert(G_NBARS <= kMaxBars, "barriers");
 constexpr uint32_t TM_S = 0, TM_P = 128, TM_DS = 256, TM_ACC = 320;
-
-struct GradMaps { CUtensorMap a1, a1r, a2, b1, b1r, b2; };   // dq: q, -, dout, k, r, v; dk: k, r, v, q, -, dout
 
 // While dS(j) is formed from dP(j), S(j + 1) runs; while P(j + 1) is formed from it, the accumulating product of
 // tile j and dP(j + 1) do. The units of B1 are freed one by one by the accumulation.
-template <bool DQ>
-__device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdArgs &b, const LatentSpan &sp, long long r0, int h,
-                                           const GradMaps &maps, unsigned char *sm)
+__device__ __forceinline__ void dq_block(const LatentArgs &a, const LatentBwdArgs &b, const LatentSpan &sp, long long r0, int h,
+                                         const BwdMaps &maps, unsigned char *sm)
 {
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long Lq = sp.q1 - sp.q0, Lk = sp.k1 - sp.k0, shift = Lk - Lq;
-    const long long row_first = (DQ ? sp.q0 : sp.k0) + r0, rows = (DQ ? Lq : Lk) - r0;     // rows: may exceed the tile
-    const long long col_first = DQ ? sp.k0 : sp.q0, cols = DQ ? Lk : Lq;
-    // tiles of the other side that some row of this one meets
-    int t_lo = 0, t_hi;
-    if (DQ) {
-        long long keys = a.causal ? min(Lk, min(r0 + TL, Lq) + shift) : Lk;
-        t_hi = keys > 0 ? (int)((keys + TL - 1) / TL) : 0;
-    } else {
-        const long long q = a.causal ? max(0LL, r0 - shift) : 0;           // first query that sees the first key here
-        t_lo = (int)(min(q, Lq) / TL);
-        t_hi = q < Lq ? (int)((Lq + TL - 1) / TL) : t_lo;
-    }
-    const int nt = t_hi - t_lo;
+    const long long Lq = sp.q1 - sp.q0, Lk = sp.k1 - sp.k0, shift = Lk - Lq, row_first = sp.q0 + r0, rows = Lq - r0;
+    // key tiles that some row of this one sees
+    const long long keys = a.causal ? min(Lk, min(r0 + TL, Lq) + shift) : Lk;
+    const int nt = keys > 0 ? (int)((keys + TL - 1) / TL) : 0;
 
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G_BAR);
-    volatile int *ctl = reinterpret_cast<volatile int *>(bars + G_NBARS);
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
-    volatile int *abort_flag = ctl + 1;
-    auto wait = [&](int x, uint32_t parity) {
-        if (mbar_try_wait(&bars[x], parity)) return true;
-        const long long t0 = clock64();
-        while (!mbar_try_wait(&bars[x], parity)) {
-            if (*abort_flag) return false;
-            if (clock64() - t0 > 2000000000LL) { *abort_flag = 1; set_status(a.status, KDA_ERR_TIMEOUT); return false; }
-        }
-        return true;
-    };
-    const int u1 = 2 + (a.R ? 1 : 0);          // units of A1 and of a tile of B1; A2 and B2 have two
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
+    volatile int *abort_flag = control(sm) + 1;
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(control(sm));
+    auto wait = [&](int x, uint32_t parity) { return wait_or_abort(&bars[x], parity, abort_flag, a.status); };
+    const int u1 = 2 + (a.R ? 1 : 0);          // units of queries and of a tile of keys; dO and values have two
 
     if (warp == W_LOAD) {
         // ============================================================================ loader
         if (elect_one() && nt > 0) {
-            // units of keys with their shared part, or of whole query rows
-            auto load1 = [&](bool key_side, const CUtensorMap *m, const CUtensorMap *mr, unsigned char *dst, uint64_t *bar, int u, int row) {
-                if (key_side && u == 2) tma_load_2d(dst, mr, bar, 0, row);
-                else tma_load_3d(dst, m, bar, u * 64, row, h);
-            };
             mbar_arrive_expect_tx(&bars[G_RES], (u1 + 2) * UNIT);
-            for (int u = 0; u < u1; ++u) load1(!DQ, &maps.a1, &maps.a1r, sm + G_A1 + u * UNIT, &bars[G_RES], u, (int)row_first);
-            for (int u = 0; u < 2; ++u) tma_load_3d(sm + G_A2 + u * UNIT, &maps.a2, &bars[G_RES], u * 64, (int)row_first, h);
+            for (int u = 0; u < u1; ++u) tma_load_3d(sm + G_A1 + u * UNIT, &maps.q, &bars[G_RES], u * 64, (int)row_first, h);
+            for (int u = 0; u < 2; ++u) tma_load_3d(sm + G_A2 + u * UNIT, &maps.d, &bars[G_RES], u * 64, (int)row_first, h);
             int s1 = 0, s2 = 0, used1 = 0, used2 = 0;
             uint32_t p1 = 0, p2 = 0;
             bool ok = true;
             for (int j = 0; j < nt && ok; ++j) {
-                const int row = (int)(col_first + (long long)(t_lo + j) * TL);
+                const int row = (int)(sp.k0 + (long long)j * TL);
                 for (int u = 0; u < u1 && ok; ++u) {
                     if (used1 >= N1) ok = wait(G_E1 + s1, p1 ^ 1);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&bars[G_F1 + s1], UNIT);
-                    load1(DQ, &maps.b1, &maps.b1r, sm + G_B1 + s1 * UNIT, &bars[G_F1 + s1], u, row);
+                    if (u < 2) tma_load_3d(sm + G_B1 + s1 * UNIT, &maps.k, &bars[G_F1 + s1], u * 64, row, h);
+                    else tma_load_2d(sm + G_B1 + s1 * UNIT, &maps.r, &bars[G_F1 + s1], 0, row);
                     ++used1;
                     if (++s1 == N1) { s1 = 0; p1 ^= 1; }
                 }
@@ -195,7 +223,7 @@ __device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdA
                     if (used2 >= N2) ok = wait(G_E2 + s2, p2 ^ 1);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&bars[G_F2 + s2], UNIT);
-                    tma_load_3d(sm + G_B2 + s2 * UNIT, &maps.b2, &bars[G_F2 + s2], u * 64, row, h);
+                    tma_load_3d(sm + G_B2 + s2 * UNIT, &maps.v, &bars[G_F2 + s2], u * 64, row, h);
                     ++used2;
                     if (++s2 == N2) { s2 = 0; p2 ^= 1; }
                 }
@@ -285,37 +313,17 @@ __device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdA
         const long long tokens = (long long)a.B * a.T;
         const float *st_lse = b.stat + (size_t)h * tokens, *st_d = st_lse + (size_t)tokens * a.H;
         asm volatile("griddepcontrol.wait;" ::: "memory");   // the statistics' kernel, whose end this block may overlap
-        float lse_r = 0.f, d_r = 0.f;                        // dq: this row's
-        if (DQ && real) { lse_r = st_lse[row_first + row]; d_r = st_d[row_first + row]; }
-        // columns this row meets: [lo, hi) of the sequence
-        // (a query that sees one key has P = 1 whatever its score: dS is 0, which dP - D would miss by a rounding)
-        long long lo = 0, hi = real ? cols : 0;
-        if (DQ) {
-            if (a.causal) hi = min(hi, r0 + row + shift + 1);
-            if (hi == 1) hi = 0;
-        } else {
-            if (a.causal) lo = r0 + row > 0 ? r0 + row - shift : 1 - shift;
-            if (Lk == 1) hi = 0;
-        }
-        const int lo_w = __reduce_max_sync(0xffffffffu, (int)max(lo, 0LL)), hi_w = __reduce_min_sync(0xffffffffu, (int)max(hi, 0LL));
-        float *stat = reinterpret_cast<float *>(sm + G_STAT);
-        // dk: each warpgroup keeps its columns' statistics, [buffer][group][lse, D][64]
-        float next = 0.f;
-        auto fetch = [&](int j) {
-            const int t = tid & 127;
-            const long long c = (long long)(t_lo + j) * TL + g * 64 + (t & 63);
-            next = c < cols ? (t < 64 ? st_lse : st_d)[col_first + c] : 0.f;
-        };
-        if (!DQ && nt > 0) fetch(0);
+        float lse_r = 0.f, d_r = 0.f;
+        if (real) { lse_r = st_lse[row_first + row]; d_r = st_d[row_first + row]; }
+        // keys this row sees (a query that sees one key has P = 1 whatever its score: dS is 0, which dP - D would miss
+        // by a rounding)
+        long long hi = real ? Lk : 0;
+        if (a.causal) hi = min(hi, r0 + row + shift + 1);
+        if (hi == 1) hi = 0;
+        const int hi_w = __reduce_min_sync(0xffffffffu, (int)max(hi, 0LL));
         for (int j = 0; j < nt; ++j) {
-            float *sj = stat + ((j & 1) * 2 + g) * 128;
-            if (!DQ) {
-                sj[tid & 127] = next;
-                if (j + 1 < nt) fetch(j + 1);
-                named_bar_sync(1 + g, 128);
-            }
-            const long long c0 = (long long)(t_lo + j) * TL + g * 64;
-            const bool edge = c0 < lo_w || c0 + 64 > hi_w;
+            const long long c0 = (long long)j * TL + g * 64;
+            const bool edge = c0 + 64 > hi_w;
             wait(G_S, j & 1);
             __syncwarp();
             tc_fence_after();
@@ -325,17 +333,10 @@ __device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdA
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars[G_SFREE]);
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                float4 l4 = make_float4(lse_r, lse_r, lse_r, lse_r);
-                if (!DQ) l4 = *reinterpret_cast<const float4 *>(sj + e);
-                p[e] = ex2(p[e] * sc - l4.x);
-                p[e + 1] = ex2(p[e + 1] * sc - l4.y);
-                p[e + 2] = ex2(p[e + 2] * sc - l4.z);
-                p[e + 3] = ex2(p[e + 3] * sc - l4.w);
-            }
-            // rows of B1 behind the sequence's end may be anything: zeros, before the accumulation reads them
+            for (int e = 0; e < 64; ++e) p[e] = ex2(p[e] * sc - lse_r);
+            // keys behind the sequence's end may be anything: zeros, before the accumulation reads them
             // (its rows are this tile's columns; each warpgroup clears its own)
-            const int valid = (int)min((long long)TL, cols - (long long)(t_lo + j) * TL);
+            const int valid = (int)min((long long)TL, Lk - (long long)j * TL);
             if (valid < (g + 1) * 64) {
                 const int from = max(valid, g * 64);
                 for (int u = 0; u < u1; ++u) {
@@ -359,21 +360,11 @@ __device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdA
                     if (lane == 0) mbar_arrive(&bars[G_PFREE]);
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    float4 d4 = make_float4(d_r, d_r, d_r, d_r);
-                    if (!DQ) d4 = *reinterpret_cast<const float4 *>(sj + 64 + half * 32 + e);
-                    float *x = p + half * 32 + e;
-                    d[e] = x[0] * (d[e] - d4.x);
-                    d[e + 1] = x[1] * (d[e + 1] - d4.y);
-                    d[e + 2] = x[2] * (d[e + 2] - d4.z);
-                    d[e + 3] = x[3] * (d[e + 3] - d4.w);
-                }
+                for (int e = 0; e < 32; ++e) d[e] = p[half * 32 + e] * (d[e] - d_r);
                 if (edge) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const long long c = c0 + half * 32 + e;
-                        if (c < lo || c >= hi) d[e] = 0.f;
-                    }
+                    for (int e = 0; e < 32; ++e)
+                        if (c0 + half * 32 + e >= hi) d[e] = 0.f;
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[half * 16 + e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
@@ -390,302 +381,354 @@ __device__ __forceinline__ void grad_block(const LatentArgs &a, const LatentBwdA
             __syncwarp();
             tc_fence_after();
         }
-        // results: chunks of 32 columns, the two warpgroups in turn
-        const size_t at = (size_t)(row_first + row) * a.H + h;
-#pragma unroll 1
-        for (int c = g * 32; c < u1 * 64; c += 64) {
-            float o[32];
-            if (nt > 0) tmem_ld32_sync(tmem + TM_ACC + lanes + c, o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = nt > 0 ? o[e] * a.scale : 0.f;
-            if (!real) continue;
-            if (!DQ && c >= kHeadDim) {
-                float4 *dst = reinterpret_cast<float4 *>(b.dr_head + at * kSharedDim + c - kHeadDim);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            } else {
-                uint4 *dst = reinterpret_cast<uint4 *>(DQ ? b.dq + at * (kHeadDim + a.R) + c : b.dk + at * kHeadDim + c);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                        pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
-            }
-        }
+        const int W = kHeadDim + a.R, half = W / 2;
+        __nv_bfloat16 *dst = b.dq + ((size_t)(row_first + quad * 32) * a.H + h) * W + g * half;
+        const size_t pitch = (size_t)a.H * W * sizeof(__nv_bfloat16);
+        const int here = (int)min(32LL, max(0LL, rows - quad * 32));
+        unsigned char *stage = sm + G_B1 + warp * 8192;       // the keys are done with
+        if (a.R) dq_result<12>(tmem + TM_ACC + lanes + g * half, nt > 0, a.scale, stage, lane, here, dst, pitch);
+        else dq_result<8>(tmem + TM_ACC + lanes + g * half, nt > 0, a.scale, stage, lane, here, dst, pitch);
     }
 }
 
-// ------------------------------------------------------------------------------------------ dv
-// The forward kernel's structure with the roles of queries and keys exchanged and lse known: two key tiles at
-// once, P^T over S^T's columns as the A operand of dv += P^T dO.
-constexpr int NVQ = 4;                        // ring of query units; dO has two tiles
-constexpr uint32_t V_A = 0, V_Q = 6 * UNIT, V_D = V_Q + NVQ * UNIT, V_STAT = V_D + 4 * UNIT, V_BAR = G_BAR;
-static_assert(V_STAT + 1024 <= V_BAR, "shared memory");
-enum { V_RES, V_QF, V_QE = V_QF + NVQ, V_DF = V_QE + NVQ, V_DE = V_DF + 2, V_S = V_DE + 2, V_PA = V_S + 2, V_PB = V_PA + 2, V_PV = V_PB + 2,
-       V_DRAIN = V_PV + 2, V_NBARS };
-static_assert((int)V_NBARS <= (int)G_NBARS, "barriers");
-constexpr uint32_t TV_S = 0, TV_O = 256;
+// ---------------------------------------------------------------------------------------- dk and dv
+// Rows of 128 keys, over query tiles. Tensor memory holds S^T (128 columns), dP^T (128), dk and dv (128 each): the
+// shared part's gradient, 64 columns more, does not fit as a sum, so its product of each tile goes to columns that
+// the tile is done with and is added up in registers. P^T and dS^T are written in bf16 over the columns they came
+// from, by each warpgroup over its own (words 0 .. 31 and 96 .. 127 of the region), which leaves columns 32 .. 95
+// of dP's region for that product.
+// One warp issues everything in this order: S(j + 1), dr(j), dk(j), dP(j + 1), dv(j + 1); the tensor cores run it in
+// order, which is what keeps S(j + 1) behind dv(j) and dP(j + 1) behind dk(j). Meanwhile the warpgroups form dS(j)
+// (beside S(j + 1)), P(j + 1) (beside dr(j) and dk(j)) and take dr(j) before dP(j + 1) overwrites it.
+// Shared memory: K (3 units) and V (2) of the block's rows, two tiles of queries, one of dO, the statistics of the
+// columns (two tiles of lse and D).
+constexpr uint32_t K_A1 = 0, K_A2 = 3 * UNIT, K_B1 = 5 * UNIT, K_B2 = K_B1 + 6 * UNIT, K_STAT = 14 * UNIT;
+static_assert(K_B2 + 2 * UNIT <= K_STAT && K_STAT + 2048 <= OFF_BAR, "shared memory");
+enum { K_RES, K_F1, K_E1 = K_F1 + 2, K_F2 = K_E1 + 2, K_E2, K_S, K_P, K_PREADY, K_DS, K_DR, K_PFREE, K_ACC, K_STATF,
+       K_DRAIN = K_STATF + 2, K_NBARS };
+static_assert((int)K_NBARS <= kMaxBars, "barriers");
+constexpr uint32_t TK_S = 0, TK_P = 128, TK_DR = TK_P + 32, TK_DK = 256, TK_DV = 384;
 
-__device__ __forceinline__ void dv_block(const LatentArgs &a, const LatentBwdArgs &b, const LatentSpan &sp, long long r0, int h,
-                                         const GradMaps &maps, unsigned char *sm)
+__device__ __forceinline__ void dkv_block(const LatentArgs &a, const LatentBwdArgs &b, const LatentSpan &sp, long long r0, int h,
+                                          const BwdMaps &maps, unsigned char *sm)
 {
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const long long Lq = sp.q1 - sp.q0, Lk = sp.k1 - sp.k0, shift = Lk - Lq, rows = Lk - r0;
-    const long long row_first = sp.k0 + r0;
-    // query tiles that see some key of tile i: from the first that sees its first key to the last
-    int first[2];
-    const int t_hi = (int)((Lq + TL - 1) / TL);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const long long q = a.causal ? max(0LL, r0 + i * TL - shift) : 0;
-        first[i] = (q < Lq && i * TL < rows) ? (int)(q / TL) : t_hi;
-    }
-    const int t_lo = min(first[0], first[1]);                  // tile 1 starts no earlier than tile 0, or has no rows
-    const int nt = t_hi - t_lo;
+    const long long Lq = sp.q1 - sp.q0, Lk = sp.k1 - sp.k0, shift = Lk - Lq, row_first = sp.k0 + r0, rows = Lk - r0;
+    // query tiles from the first that sees this tile's first key
+    const long long q_lo = a.causal ? max(0LL, r0 - shift) : 0;
+    const int t_lo = (int)(min(q_lo, Lq) / TL), nt = q_lo < Lq ? (int)((Lq + TL - 1) / TL) - t_lo : 0;
 
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + V_BAR);
-    volatile int *ctl = reinterpret_cast<volatile int *>(bars + G_NBARS);
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
-    volatile int *abort_flag = ctl + 1;
-    auto wait = [&](int x, uint32_t parity) {
-        if (mbar_try_wait(&bars[x], parity)) return true;
-        const long long t0 = clock64();
-        while (!mbar_try_wait(&bars[x], parity)) {
-            if (*abort_flag) return false;
-            if (clock64() - t0 > 2000000000LL) { *abort_flag = 1; set_status(a.status, KDA_ERR_TIMEOUT); return false; }
-        }
-        return true;
-    };
-    const int u1 = 2 + (a.R ? 1 : 0);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
+    volatile int *abort_flag = control(sm) + 1;
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(control(sm));
+    auto wait = [&](int x, uint32_t parity) { return wait_or_abort(&bars[x], parity, abort_flag, a.status); };
+    const bool has_r = a.R != 0;
+    const int u1 = 2 + (has_r ? 1 : 0);
 
     if (warp == W_LOAD) {
         // ============================================================================ loader
         if (elect_one() && nt > 0) {
-            mbar_arrive_expect_tx(&bars[V_RES], 2 * u1 * UNIT);
-            for (int i = 0; i < 2; ++i)
-                for (int u = 0; u < u1; ++u) {
-                    unsigned char *dst = sm + V_A + (i * 3 + u) * UNIT;
-                    if (u == 2) tma_load_2d(dst, &maps.a1r, &bars[V_RES], 0, (int)(row_first + i * TL));
-                    else tma_load_3d(dst, &maps.a1, &bars[V_RES], u * 64, (int)(row_first + i * TL), h);
-                }
-            int s = 0, used = 0, j = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (; j < nt; ++j) {
-                const int row = (int)(sp.q0 + (long long)(t_lo + j) * TL), b = j & 1;
-                for (int u = 0; u < u1; ++u) {
-                    if (used >= NVQ && !(ok = wait(V_QE + s, ph ^ 1))) break;
-                    mbar_arrive_expect_tx(&bars[V_QF + s], UNIT);
-                    tma_load_3d(sm + V_Q + s * UNIT, &maps.b1, &bars[V_QF + s], u * 64, row, h);
-                    ++used;
-                    if (++s == NVQ) { s = 0; ph ^= 1; }
-                }
-                if (!ok || (j >= 2 && !(ok = wait(V_DE + b, ((j >> 1) - 1) & 1)))) break;
-                unsigned char *dst = sm + V_D + b * 2 * UNIT;
-                mbar_arrive_expect_tx(&bars[V_DF + b], 2 * UNIT);
-                tma_load_3d(dst, &maps.b2, &bars[V_DF + b], 0, row, h);
-                tma_load_3d(dst + UNIT, &maps.b2, &bars[V_DF + b], 64, row, h);
+            mbar_arrive_expect_tx(&bars[K_RES], (u1 + 2) * UNIT);
+            for (int u = 0; u < 2; ++u) {
+                tma_load_3d(sm + K_A1 + u * UNIT, &maps.k, &bars[K_RES], u * 64, (int)row_first, h);
+                tma_load_3d(sm + K_A2 + u * UNIT, &maps.v, &bars[K_RES], u * 64, (int)row_first, h);
             }
-            if (!ok) {
-                mbar_wait(&bars[V_RES], 0, 100000000LL);
-                for (int x = max(0, used - NVQ); x < used; ++x) mbar_wait(&bars[V_QF + x % NVQ], (x / NVQ) & 1, 100000000LL);
-                for (int x = max(0, j - 2); x < j; ++x) mbar_wait(&bars[V_DF + (x & 1)], (x >> 1) & 1, 100000000LL);
+            if (has_r) tma_load_2d(sm + K_A1 + 2 * UNIT, &maps.r, &bars[K_RES], 0, (int)row_first);
+            bool ok = true;
+            int j = 0;
+            for (; j < nt; ++j) {
+                const int row = (int)(sp.q0 + (long long)(t_lo + j) * TL), x = j & 1;
+                if (j >= 2 && !(ok = wait(K_E1 + x, ((j >> 1) - 1) & 1))) break;
+                mbar_arrive_expect_tx(&bars[K_F1 + x], u1 * UNIT);
+                for (int u = 0; u < u1; ++u) tma_load_3d(sm + K_B1 + (x * 3 + u) * UNIT, &maps.q, &bars[K_F1 + x], u * 64, row, h);
+                if (j >= 1 && !(ok = wait(K_E2, (j - 1) & 1))) break;
+                mbar_arrive_expect_tx(&bars[K_F2], 2 * UNIT);
+                for (int u = 0; u < 2; ++u) tma_load_3d(sm + K_B2 + u * UNIT, &maps.d, &bars[K_F2], u * 64, row, h);
+            }
+            if (!ok) {                          // a wait ran out: what is in flight lands before the block ends
+                mbar_wait(&bars[K_RES], 0, 100000000LL);
+                for (int x = max(0, j - 1); x <= j && x < nt; ++x) mbar_wait(&bars[K_F1 + (x & 1)], (x >> 1) & 1, 100000000LL);
+                if (j > 0) mbar_wait(&bars[K_F2], (j - 1) & 1, 100000000LL);
             }
         }
     } else if (warp == W_MMA) {
-        // ======================================================================== MMA issuer, as in the forward kernel
+        // ======================================================================== MMA issuer
         const bool el = elect_one();
-        constexpr uint32_t id_s = idesc_bf16(TL, TL, 0, 0), id_o = idesc_bf16(TL, 128, 0, 1);
+        constexpr uint32_t id_s = idesc_bf16(TL, TL, 0, 0), id_a = idesc_bf16(TL, 128, 0, 1), id_r = idesc_bf16(TL, 64, 0, 1);
         constexpr uint32_t hi = desc_hi(1024, SW_128B);
-        const uint32_t a_lo = desc_lo(sbase + V_A, 16), q_lo = desc_lo(sbase + V_Q, 16), d_lo = desc_lo(sbase + V_D, UNIT);
+        const uint32_t a1_lo = desc_lo(sbase + K_A1, 16), a2_lo = desc_lo(sbase + K_A2, 16);
+        const uint32_t b1_lo = desc_lo(sbase + K_B1, 16), b2_lo = desc_lo(sbase + K_B2, 16);     // as K-major operands
+        const uint32_t q_lo_mn = desc_lo(sbase + K_B1, UNIT), d_lo_mn = desc_lo(sbase + K_B2, UNIT);
         const int ntu = __reduce_max_sync(0xffffffffu, nt);
-        const int f0 = __reduce_max_sync(0xffffffffu, first[0] - t_lo), f1 = __reduce_max_sync(0xffffffffu, first[1] - t_lo);
-        int qs = 0;
-        uint32_t qp = 0;
-        auto scores = [&](int i, bool mine) {
-            int x = qs;
-            uint32_t ph = qp;
-            for (int u = 0; u < u1; ++u) {
-                if (i == 0) { wait(V_QF + x, ph); tc_fence_after(); }
-                if (el) {
-                    if (mine) {
-                        const uint32_t k = a_lo + (i * 3 + u) * (UNIT / 16), q = q_lo + x * (UNIT / 16), d = tmem + TV_S + i * 128;
+        auto scores = [&](int j) {
+            wait(K_F1 + (j & 1), (j >> 1) & 1);
+            tc_fence_after();
+            if (el) {
+                const uint32_t y = b1_lo + (j & 1) * (3 * UNIT / 16);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) umma_ss(d, desc64(k + e * 2, hi), desc64(q + e * 2, hi), id_s, (e > 0 || u > 0) ? 1 : 0);
-                    }
-                    if (i == 1) umma_commit(&bars[V_QE + x]);
+                for (int e = 0; e < 8; ++e)
+                    umma_ss(tmem + TK_S, desc64(a1_lo + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi),
+                            desc64(y + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), id_s, e > 0 ? 1 : 0);
+                if (has_r) {
+#pragma unroll
+                    for (int e = 8; e < 12; ++e)
+                        umma_ss(tmem + TK_S, desc64(a1_lo + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi),
+                                desc64(y + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), id_s, 1);
                 }
-                if (++x == NVQ) { x = 0; ph ^= 1; }
+                umma_commit(&bars[K_S]);
             }
-            if (el && mine) umma_commit(&bars[V_S + i]);
-            if (i == 1) { qs = x; qp = ph; }
+        };
+        auto dp = [&](int j) {
+            wait(K_F2, j & 1);
+            tc_fence_after();
+            if (el) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    umma_ss(tmem + TK_P, desc64(a2_lo + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi),
+                            desc64(b2_lo + (e >> 2) * (UNIT / 16) + (e & 3) * 2, hi), id_s, e > 0 ? 1 : 0);
+                umma_commit(&bars[K_P]);
+            }
         };
         if (ntu > 0) {
-            wait(V_RES, 0);
-            scores(0, f0 == 0);
-            scores(1, f1 == 0);
+            wait(K_RES, 0);
+            scores(0);
+            dp(0);
         }
         for (int j = 0; j < ntu; ++j) {
-            const int b = j & 1;
-            const bool more = j + 1 < ntu;
-            wait(V_DF + b, (j >> 1) & 1);
+            const uint32_t more = j > 0 ? 1 : 0;
+            wait(K_PREADY, j & 1);
+            tc_fence_after();
+            if (el) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int f = i ? f1 : f0;
-                if (j >= f) {
-                    const uint32_t d = tmem + TV_O + i * 128, p = tmem + TV_S + i * 128, v = d_lo + b * (2 * UNIT / 16);
+                for (int e = 0; e < 8; ++e)
+                    umma_ts(tmem + TK_DV, tmem + TK_S + (e < 4 ? e * 8 : 64 + e * 8), desc64(d_lo_mn + e * 128, hi), id_a, e > 0 ? 1 : more);
+                umma_commit(&bars[K_E2]);
+            }
+            if (j + 1 < ntu) scores(j + 1);
+            wait(K_DS, j & 1);
+            tc_fence_after();
+            if (el) {
+                const uint32_t y = q_lo_mn + (j & 1) * (3 * UNIT / 16);
+                if (has_r) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        wait((half ? V_PB : V_PA) + i, (j - f) & 1);
-                        tc_fence_after();
-                        if (el) {
-#pragma unroll
-                            for (int e = half * 4; e < half * 4 + 4; ++e)
-                                umma_ts(d, p + e * 8, desc64(v + e * 128, hi), id_o, (e > 0 || j > f) ? 1 : 0);
-                        }
-                    }
-                    if (el) umma_commit(&bars[V_PV + i]);
+                    for (int e = 0; e < 8; ++e)
+                        umma_ts(tmem + TK_DR, tmem + TK_P + (e < 4 ? e * 8 : 64 + e * 8), desc64(y + 2 * (UNIT / 16) + e * 128, hi), id_r, e > 0 ? 1 : 0);
+                    umma_commit(&bars[K_DR]);
                 }
-                if (i == 1 && el) umma_commit(&bars[V_DE + b]);
-                if (more) scores(i, j + 1 >= f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    umma_ts(tmem + TK_DK, tmem + TK_P + (e < 4 ? e * 8 : 64 + e * 8), desc64(y + e * 128, hi), id_a, e > 0 ? 1 : more);
+                umma_commit(&bars[K_E1 + (j & 1)]);
+                umma_commit(&bars[K_ACC]);
+            }
+            if (j + 1 < ntu) {
+                wait(K_PFREE, j & 1);
+                dp(j + 1);
             }
             if (*abort_flag) break;
         }
         if (el) {
-            umma_commit(&bars[V_DRAIN]);
-            if (!mbar_wait(&bars[V_DRAIN], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
+            umma_commit(&bars[K_DRAIN]);
+            if (!mbar_wait(&bars[K_DRAIN], 0, 100000000LL)) set_status(a.status, KDA_ERR_TIMEOUT);
+        }
+    } else if (warp == W_MMA + 1) {
+        // ====================================================== the columns' statistics, [buffer][group][lse, D][64]
+        asm volatile("griddepcontrol.wait;" ::: "memory");   // their kernel, whose end this block may overlap
+        const long long tokens = (long long)a.B * a.T;
+        const float *lse = b.stat + (size_t)h * tokens + sp.q0, *d = lse + (size_t)tokens * a.H;
+        float *stat = reinterpret_cast<float *>(sm + K_STAT);
+        for (int j = 0; j < nt; ++j) {
+            float x[4], y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const long long c = (long long)(t_lo + j) * TL + e * 32 + lane;
+                x[e] = c < Lq ? lse[c] : 0.f;
+                y[e] = c < Lq ? d[c] : 0.f;
+            }
+            if (j >= 2) { wait(K_DS, j & 1); __syncwarp(); }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float *to = stat + (j & 1) * 256 + (e >> 1) * 128 + (e & 1) * 32 + lane;
+                to[0] = x[e];
+                to[64] = y[e];
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[K_STATF + (j & 1)]);
         }
     } else if (warp < W_LOAD) {
-        // ============================================================================ P
-        const int i = warp >> 2, quad = warp & 3;
+        // ============================================================================ P and dS
+        // Lane = key; the two warpgroups share the columns (queries).
+        const int g = warp >> 2, quad = warp & 3;
         const uint32_t lanes = (uint32_t)quad << 21;
-        const uint32_t ts = tmem + TV_S + i * 128 + lanes, to = tmem + TV_O + i * 128 + lanes;
-        const int row = i * TL + quad * 32 + lane;                  // of the block's 256 keys
+        const int row = quad * 32 + lane;
         const bool real = row < rows;
         const float sc = a.scale * 1.44269504088896341f;
-        const float *st_lse = b.stat + (size_t)h * ((long long)a.B * a.T);
-        asm volatile("griddepcontrol.wait;" ::: "memory");          // the statistics' kernel
-        const long long lo = a.causal ? r0 + row - shift : 0;       // first query that sees this key
-        const int lo_w = __reduce_max_sync(0xffffffffu, (int)max(lo, 0LL));
-        float *stat = reinterpret_cast<float *>(sm + V_STAT) + i * TL;
-        const int f = first[i];
-        float next = 0.f;
-        auto fetch = [&](int tile) {
-            const long long c = (long long)tile * TL + (tid & 127);
-            next = c < Lq ? -st_lse[sp.q0 + c] : -INFINITY;
-        };
-        if (f < t_hi) fetch(f);
-        for (int tile = f; tile < t_hi; ++tile) {
-            const int j = tile - f;
-            named_bar_sync(1 + i, 128);                             // the last tile's statistics are read
-            stat[tid & 127] = next;
-            if (tile + 1 < t_hi) fetch(tile + 1);
-            named_bar_sync(1 + i, 128);
-            const long long c0 = (long long)tile * TL;
-            const bool edge = c0 < lo_w || c0 + TL > Lq;
-            wait(V_S + i, j & 1);
+        // queries that see this key: [lo, hi) of the sequence; [ds_lo, hi) with a gradient through the score (a query
+        // that sees one key has none)
+        const long long lo = a.causal ? r0 + row - shift : 0, hi = real ? Lq : 0;
+        const long long ds_lo = Lk == 1 ? hi : a.causal && r0 + row == 0 ? max(lo, 1 - shift) : lo;
+        const int lo_w = __reduce_max_sync(0xffffffffu, (int)max(ds_lo, 0LL)), hi_w = __reduce_min_sync(0xffffffffu, (int)hi);
+        const float *stat = reinterpret_cast<const float *>(sm + K_STAT) + g * 128;
+        float dr[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) dr[e] = 0.f;
+        auto take_dr = [&](int j) {                          // the shared part's product of tile j
+            wait(K_DR, j & 1);
             __syncwarp();
             tc_fence_after();
-            // gradients of rows behind the sequence's last query may be anything: zeros, before the product reads them
-            // (behind the wait for the scores: the ring slots' earlier uses are over by then, so the parity is this use's)
-            if (c0 + TL > Lq) {
-                const int valid = (int)(Lq - c0), x = tile - t_lo;
-                wait(V_DF + (x & 1), (x >> 1) & 1);
-                for (int u = 0; u < 2; ++u) {
-                    unsigned char *un = sm + V_D + ((x & 1) * 2 + u) * UNIT;
-                    for (int e = quad * 32 + lane; e < (TL - valid) * 8; e += 128)
-                        *reinterpret_cast<uint4 *>(un + valid * 128 + e * 16) = make_uint4(0, 0, 0, 0);
+            float x[32];
+            tmem_ld32_sync(tmem + TK_DR + lanes + g * 32, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) dr[e] += x[e];
+        };
+        for (int j = 0; j < nt; ++j) {
+            const float *sj = stat + (j & 1) * 256;
+            const long long c0 = (long long)(t_lo + j) * TL + g * 64;
+            const bool edge = c0 < lo_w || c0 + 64 > hi_w;
+            wait(K_STATF + (j & 1), (j >> 1) & 1);
+            wait(K_S, j & 1);
+            __syncwarp();
+            tc_fence_after();
+            float p[64];
+            tmem_ld64_sync(tmem + TK_S + lanes + g * 64, p);
+            auto exps = [&](int from) {
+#pragma unroll
+                for (int e = from; e < from + 32; e += 4) {
+                    const float4 l4 = *reinterpret_cast<const float4 *>(sj + e);
+                    p[e] = ex2(p[e] * sc - l4.x);
+                    p[e + 1] = ex2(p[e + 1] * sc - l4.y);
+                    p[e + 2] = ex2(p[e + 2] * sc - l4.z);
+                    p[e + 3] = ex2(p[e + 3] * sc - l4.w);
+                }
+            };
+            exps(0);
+            if (j > 0) {
+                if (has_r) take_dr(j - 1);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[K_PFREE]);
+            }
+            exps(32);
+            if (edge) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (c0 + e < lo || c0 + e >= hi) p[e] = 0.f;
+            }
+            // queries and gradients behind the sequence's end may be anything: zeros, before the products over them
+            // (each warpgroup clears its own columns' rows; the scores' wait put both copies' earlier uses behind)
+            const int valid = (int)min((long long)TL, Lq - (long long)(t_lo + j) * TL);
+            if (valid < (g + 1) * 64) {
+                const int from = max(valid, g * 64);
+                wait(K_F2, j & 1);
+                for (int u = 0; u < u1 + 2; ++u) {
+                    unsigned char *un = sm + (u < u1 ? K_B1 + ((j & 1) * 3 + u) * UNIT : K_B2 + (u - u1) * UNIT);
+                    for (int e = tid & 127; e < ((g + 1) * 64 - from) * 8; e += 128)
+                        *reinterpret_cast<uint4 *>(un + from * 128 + e * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
             }
+            uint32_t w[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
+            tmem_st32(tmem + TK_S + lanes + g * 96, w);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[K_PREADY]);
+            wait(K_P, j & 1);
+            __syncwarp();
+            tc_fence_after();
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                float s[64];
-                tmem_ld64_sync(ts + half * 64, s);
+                float d[32];
+                tmem_ld32_sync(tmem + TK_P + lanes + g * 64 + half * 32, d);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 d4 = *reinterpret_cast<const float4 *>(sj + 64 + half * 32 + e);
+                    const float *x = p + half * 32 + e;
+                    d[e] = x[0] * (d[e] - d4.x);
+                    d[e + 1] = x[1] * (d[e + 1] - d4.y);
+                    d[e + 2] = x[2] * (d[e + 2] - d4.z);
+                    d[e + 3] = x[3] * (d[e + 3] - d4.w);
+                }
                 if (edge) {
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        const long long c = c0 + half * 64 + e;
-                        if (c < lo || c >= Lq) s[e] = -INFINITY;
+                    for (int e = 0; e < 32; ++e) {
+                        const long long c = c0 + half * 32 + e;
+                        if (c < ds_lo || c >= hi) d[e] = 0.f;
                     }
                 }
-                uint32_t w[32];
-                const uint64_t sc2 = f2(sc, sc);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float4 l4 = *reinterpret_cast<const float4 *>(stat + half * 64 + 2 * e);       // minus lse
-                    float x0, x1, x2, x3;
-                    f2_split(f2_fma(f2(s[2 * e], s[2 * e + 1]), sc2, f2(l4.x, l4.y)), x0, x1);
-                    f2_split(f2_fma(f2(s[2 * e + 2], s[2 * e + 3]), sc2, f2(l4.z, l4.w)), x2, x3);
-                    w[e] = pack_bf16x2(ex2(x0), ex2(x1));
-                    w[e + 1] = pack_bf16x2(ex2(x2), ex2(x3));
-                }
-                tmem_st32(ts + half * 32, w);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[(half ? V_PB : V_PA) + i]);
+                for (int e = 0; e < 16; ++e) w[half * 16 + e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
             }
+            tmem_st32(tmem + TK_P + lanes + g * 96, w);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[K_DS]);
         }
-        const int cnt = t_hi - f;
-        if (cnt > 0) {
-            wait(V_PV + i, (cnt - 1) & 1);
+        if (nt > 0) {
+            if (has_r) take_dr(nt - 1);
+            wait(K_ACC, (nt - 1) & 1);                       // and dv's products, which were issued before
             __syncwarp();
             tc_fence_after();
         }
-        const size_t at = (size_t)(row_first + row) * a.H + h;
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-            float o[32];
-            if (cnt > 0) tmem_ld32_sync(to + c, o);
-            uint32_t w[16];
+        const size_t at = (size_t)(row_first + quad * 32) * a.H + h;
+        const int here = (int)min(32LL, max(0LL, rows - quad * 32));
+        unsigned char *stage = sm + K_B1 + warp * 16384;     // queries and dO are done with
+        if (has_r) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = cnt > 0 ? pack_bf16x2(o[2 * e], o[2 * e + 1]) : 0u;
-            if (real) {
-                uint4 *dst = reinterpret_cast<uint4 *>(b.dv + at * kHeadDim + c);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) {
+                const float4 x = make_float4(dr[4 * e] * a.scale, dr[4 * e + 1] * a.scale, dr[4 * e + 2] * a.scale, dr[4 * e + 3] * a.scale);
+                *reinterpret_cast<float4 *>(stage + lane * 144 + e * 16) = x;
             }
+            store_stage<8>(stage, lane, here, b.dr_head + at * kSharedDim + g * 32, (size_t)a.H * kSharedDim * sizeof(float));
         }
+        // one warpgroup writes dk, the other dv
+        const float f = g ? 1.f : a.scale;
+#pragma unroll
+        for (int c = 0; c < kHeadDim; c += 32) {
+            float o[32];
+            if (nt > 0) tmem_ld32_sync(tmem + (g ? TK_DV : TK_DK) + lanes + c, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = nt > 0 ? o[e] * f : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) stage_piece<16>(stage, lane, c / 8 + e, pack8(o + 8 * e));
+        }
+        store_stage<16>(stage, lane, here, (g ? b.dv : b.dk) + at * kHeadDim, (size_t)a.H * kHeadDim * sizeof(__nv_bfloat16));
     }
 }
 
-// One launch for the three: blocks of dv, then of dk, then of dq, so that a kind's last blocks do not leave the GPU
-// idle and the longest blocks (dv: two tiles of rows) are not the last, each kind from a sequence's longest row of tiles
-// to its shortest. (Ranking the tiles of all sequences, as the forward kernel does, cost these shorter blocks more than
-// it gave: 105 us became 120, 6 sequences x 8 heads.)
+// One launch for both: blocks of dk and dv, then of dq, so that the first kind's last blocks do not leave the GPU idle,
+// each kind from a sequence's longest row of tiles to its shortest. (Ranking the tiles of all sequences, as the forward
+// kernel does, cost these shorter blocks more than it gave: 105 us became 120, 6 sequences x 8 heads.)
 __global__ void __launch_bounds__(NT, 1)
-latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_slots, long long v_slots,
-                  const __grid_constant__ GradMaps mq, const __grid_constant__ GradMaps mk)
+latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_slots, const __grid_constant__ BwdMaps maps)
 {
     extern __shared__ __align__(1024) unsigned char sm[];
     if (blockIdx.x == 0 && a.T == 0) check_call(a);              // (else the statistics' kernel does)
     const int h = blockIdx.x % a.H, warp = threadIdx.x >> 5;
     long long x = blockIdx.x / a.H;
-    int kind = 2;                              // 0 dq, 1 dk, 2 dv
-    if (x >= v_slots) { x -= v_slots; kind = 1; }
-    if (kind == 1 && x >= k_slots) { x -= k_slots; kind = 0; }
-    const bool keys = kind > 0;
+    const bool keys = x < k_slots;
+    if (!keys) x = q_slots - 1 - (x - k_slots);
     // tensor memory and barriers, beside the search for the block's tile
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + G_BAR);
-    volatile int *ctl = reinterpret_cast<volatile int *>(bars + G_NBARS);      // [0] tensor memory, [1] abort
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
+    volatile int *ctl = control(sm);
     if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
     if (warp == W_LOAD && elect_one()) {
-        for (int i = 0; i < (kind == 2 ? V_NBARS : G_NBARS); ++i) {
-            const bool by_warps = kind == 2 ? i >= V_PA && i < V_PV : i == G_SFREE || i == G_PFREE || i == G_DS;
-            mbar_init(&bars[i], by_warps ? (kind == 2 ? 4 : 8) : 1);
+        for (int i = 0; i < (keys ? (int)K_NBARS : (int)G_NBARS); ++i) {
+            const bool by_warps = keys ? i == K_PREADY || i == K_DS || i == K_PFREE : i == G_SFREE || i == G_PFREE || i == G_DS;
+            mbar_init(&bars[i], by_warps ? 8 : 1);
         }
         ctl[1] = 0;
         fence_mbar_init();
-        const GradMaps &m = kind == 0 ? mq : mk;
-        if (a.T > 0 && a.Tk > 0) { tma_prefetch_desc(&m.a1); tma_prefetch_desc(&m.a2); tma_prefetch_desc(&m.b1); tma_prefetch_desc(&m.b2); }
+        if (a.T > 0 && a.Tk > 0) { tma_prefetch_desc(&maps.q); tma_prefetch_desc(&maps.k); tma_prefetch_desc(&maps.v); tma_prefetch_desc(&maps.d); }
     }
-    const int tile = kind == 2 ? 2 * TL : TL;
-    const long long slots = kind == 0 ? q_slots : kind == 1 ? k_slots : v_slots;
     LatentSpan sp;
     long long r0;
     int n;
-    bool some = latent_slot(keys ? a.cu_k : a.cu_q, a, keys ? a.Tk : a.T, keys, tile, keys ? x : slots - 1 - x, &n, &sp, &r0);
+    bool some = latent_slot(keys ? a.cu_k : a.cu_q, a, keys ? a.Tk : a.T, keys, TL, x, &n, &sp, &r0);
     if (smem_u32(sm) & 1023u) {                // swizzled tiles need it (it holds)
         if (threadIdx.x == 0) set_status(a.status, KDA_ERR_CUDA);
         some = false;
@@ -697,12 +740,10 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
     if (!some) {
         // no block ends before the statistics' kernel has: what follows this kernel must not overtake that one
         asm volatile("griddepcontrol.wait;" ::: "memory");
-    } else if (kind == 0) {
-        grad_block<true>(a, b, sp, r0, h, mq, sm);
-    } else if (kind == 1) {
-        grad_block<false>(a, b, sp, r0, h, mk, sm);
+    } else if (keys) {
+        dkv_block(a, b, sp, r0, h, maps, sm);
     } else {
-        dv_block(a, b, sp, r0, h, mk, sm);
+        dq_block(a, b, sp, r0, h, maps, sm);
     }
     tc_fence_before();
     __syncthreads();
@@ -735,21 +776,18 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
 {
     const long long tokens = (long long)a.B * a.T, keys = (long long)a.B * a.Tk;
     const long long q_slots = tokens > 0 ? tokens / TL + a.N : 0, k_slots = keys > 0 ? keys / TL + a.N : 0;
-    const long long v_slots = keys > 0 ? keys / (2 * TL) + a.N : 0;
-    if ((q_slots + k_slots + v_slots) * a.H > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if ((q_slots + k_slots) * a.H > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int W = kHeadDim + a.R;
-    CUtensorMap q = {}, k = {}, r = {}, v = {}, d = {};          // an empty side's tiles are never copied
-    if (tokens > 0 && (!bf16_heads_map(&q, a.q, W, a.H, tokens, W, (long long)a.H * W, 64, TL) ||
-                       !bf16_heads_map(&d, b.dout, kHeadDim, a.H, tokens, kHeadDim, (long long)a.H * kHeadDim, 64, TL)))
+    BwdMaps m = {};                                               // an empty side's tiles are never copied
+    if (tokens > 0 && (!bf16_heads_map(&m.q, a.q, W, a.H, tokens, W, (long long)a.H * W, 64, TL) ||
+                       !bf16_heads_map(&m.d, b.dout, kHeadDim, a.H, tokens, kHeadDim, (long long)a.H * kHeadDim, 64, TL)))
         return cudaErrorNotSupported;
-    if (keys > 0 && (!bf16_heads_map(&k, a.k, kHeadDim, a.H, keys, a.k_head, a.k_tok, 64, TL) ||
-                     !bf16_heads_map(&v, a.v, kHeadDim, a.H, keys, a.v_head, a.v_tok, 64, TL) ||
-                     (a.R && !bf16_rows_map(&r, a.r, kSharedDim, keys, a.r_tok, 64, TL))))
+    if (keys > 0 && (!bf16_heads_map(&m.k, a.k, kHeadDim, a.H, keys, a.k_head, a.k_tok, 64, TL) ||
+                     !bf16_heads_map(&m.v, a.v, kHeadDim, a.H, keys, a.v_head, a.v_tok, 64, TL) ||
+                     (a.R && !bf16_rows_map(&m.r, a.r, kSharedDim, keys, a.r_tok, 64, TL))))
         return cudaErrorNotSupported;
-    constexpr uint32_t smem = G_END;
-    const cudaError_t e = cudaFuncSetAttribute(latent_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(latent_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return e;
-    const GradMaps mq = {q, q, d, k, r, v}, mk = {k, r, v, q, q, d};
     if (tokens > 0)
         latent_stat_kernel<<<dim3((unsigned)((tokens + 15) / 16), a.H), 256, 0, stream>>>(a, b.dout, b.stat, tokens);
     // its blocks set up and load their first tiles while the statistics are being finished
@@ -757,13 +795,13 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((q_slots + k_slots + v_slots) * a.H));
+    cfg.gridDim = dim3((unsigned)((q_slots + k_slots) * a.H));
     cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = SMEM;
     cfg.stream = stream;
     cfg.attrs = &at;
     cfg.numAttrs = tokens > 0 ? 1 : 0;
-    const cudaError_t e2 = cudaLaunchKernelEx(&cfg, latent_bwd_kernel, a, b, q_slots, k_slots, v_slots, mq, mk);
+    const cudaError_t e2 = cudaLaunchKernelEx(&cfg, latent_bwd_kernel, a, b, q_slots, k_slots, m);
     if (e2 != cudaSuccess) return e2;
     if (a.R && keys > 0) latent_dr_kernel<<<(unsigned)((keys + 15) / 16), 256, 0, stream>>>(b.dr_head, b.dr, keys, a.H);
     return cudaGetLastError();
