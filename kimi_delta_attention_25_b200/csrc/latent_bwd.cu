@@ -324,6 +324,7 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, const LatentBwdArg
         for (int j = 0; j < nt; ++j) {
             const long long c0 = (long long)j * TL + g * 64;
             const bool edge = c0 + 64 > hi_w;
+            const int hi_e = (int)max(0LL, min(64LL, hi - c0));
             wait(G_S, j & 1);
             __syncwarp();
             tc_fence_after();
@@ -364,7 +365,7 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, const LatentBwdArg
                 if (edge) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (c0 + half * 32 + e >= hi) d[e] = 0.f;
+                        if (half * 32 + e >= hi_e) d[e] = 0.f;
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[half * 16 + e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
@@ -586,6 +587,8 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, const LatentBwdAr
             const float *sj = stat + (j & 1) * 256;
             const long long c0 = (long long)(t_lo + j) * TL + g * 64;
             const bool edge = c0 < lo_w || c0 + 64 > hi_w;
+            const int lo_e = (int)max(0LL, min(64LL, lo - c0)), hi_e = (int)max(0LL, min(64LL, hi - c0));
+            const int ds_lo_e = (int)max(0LL, min(64LL, ds_lo - c0));
             wait(K_STATF + (j & 1), (j >> 1) & 1);
             wait(K_S, j & 1);
             __syncwarp();
@@ -613,7 +616,7 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, const LatentBwdAr
             if (edge) {
 #pragma unroll
                 for (int e = 0; e < 64; ++e)
-                    if (c0 + e < lo || c0 + e >= hi) p[e] = 0.f;
+                    if (e < lo_e || e >= hi_e) p[e] = 0.f;
             }
             // queries and gradients behind the sequence's end may be anything: zeros, before the products over them
             // (each warpgroup clears its own columns' rows; the scores' wait put both copies' earlier uses behind)
@@ -654,10 +657,8 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, const LatentBwdAr
                 }
                 if (edge) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const long long c = c0 + half * 32 + e;
-                        if (c < ds_lo || c >= hi) d[e] = 0.f;
-                    }
+                    for (int e = 0; e < 32; ++e)
+                        if (half * 32 + e < ds_lo_e || half * 32 + e >= hi_e) d[e] = 0.f;
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) w[half * 16 + e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
