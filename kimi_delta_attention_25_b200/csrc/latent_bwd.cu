@@ -37,28 +37,38 @@ __device__ __forceinline__ float dot8(const uint4 &x, const uint4 &y)
 }
 
 // lse in the log2 domain and D_i = do_i . o_i as [H][tokens] (the dk and dv blocks read them along the
-// tokens): one warp per head and two tokens, half a warp to a row.
+// tokens): one warp per head and eight tokens, half a warp to a row, all its rows on their way at once (two tokens to a
+// warp took twice the time).
 // `out` has been rounded to bf16, which moves D by up to 2^-8 of |do| . |o|. Beside the rounding of dS itself that
 // matters where a row sees few keys (dS is then a difference of nearly equal values, and o as large as v): rows
 // that see at most kShortRow keys get D = sum_j P_ij dP_ij instead, from the same sums in fp32.
-constexpr int kShortRow = 16;
+constexpr int kShortRow = 16, kStatTokens = 8;
+static_assert(8 * kStatTokens <= 64, "a block's tokens, a bit each");
 __global__ void __launch_bounds__(256) latent_stat_kernel(LatentArgs a, const __nv_bfloat16 *__restrict__ dout, float *__restrict__ stat,
                                                           long long tokens)
 {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && blockIdx.y == 0) check_call(a);
-    const int H = a.H, lane = threadIdx.x & 31, h = blockIdx.y;
-    const long long t0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 2, tok = t0 + (lane >> 4);
-    if (t0 >= tokens) return;
-    const bool real = tok < tokens;
-    uint4 o = make_uint4(0, 0, 0, 0), od = o;
-    float l = 0.f;
-    if (real) {
-        o = reinterpret_cast<const uint4 *>(a.out + (tok * H + h) * kHeadDim)[lane & 15];
-        od = reinterpret_cast<const uint4 *>(dout + (tok * H + h) * kHeadDim)[lane & 15];
-        l = a.lse[tok * H + h];
+    __shared__ uint32_t short_of[8];           // bit = token of that warp that sees 2 to kShortRow keys
+    __shared__ long long short_k0[8 * kStatTokens];
+    __shared__ int short_keys[8 * kStatTokens];
+    __shared__ float short_lse[8 * kStatTokens];
+    const int H = a.H, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
+    const long long block0 = (long long)blockIdx.x * 8 * kStatTokens, t0 = block0 + warp * kStatTokens, tok = t0 + (lane & (kStatTokens - 1));
+    uint4 o[kStatTokens / 2], od[kStatTokens / 2];
+#pragma unroll
+    for (int u = 0; u < kStatTokens / 2; ++u) {
+        const long long t = t0 + 2 * u + (lane >> 4);
+        o[u] = od[u] = make_uint4(0, 0, 0, 0);
+        if (t < tokens) {
+            o[u] = reinterpret_cast<const uint4 *>(a.out + (t * H + h) * kHeadDim)[lane & 15];
+            od[u] = reinterpret_cast<const uint4 *>(dout + (t * H + h) * kHeadDim)[lane & 15];
+        }
     }
-    long long k0 = 0, seen = 0;                // the keys that this half warp's token sees
+    // from here a lane has a token: its lse, the keys that it sees, its sum
+    const bool real = lane < kStatTokens && tok < tokens;
+    const float l = real ? a.lse[tok * H + h] : 0.f;
+    long long k0 = 0, seen = 0;
     if (real) {
         const int n = latent_sequence(a.cu_q, a.N, a.T, tok);
         LatentSpan s;
@@ -68,15 +78,39 @@ __global__ void __launch_bounds__(256) latent_stat_kernel(LatentArgs a, const __
             if (a.causal) seen = min(seen, tok - s.q0 + (s.k1 - s.k0) - (s.q1 - s.q0) + 1);
         }
     }
-    float mine = dot8(o, od);
+    float mine = 0.f;
 #pragma unroll
-    for (int m = 8; m > 0; m >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, m);
-    for (uint32_t todo = __ballot_sync(0xffffffffu, (lane & 15) == 0 && seen > 1 && seen <= kShortRow); todo; todo &= todo - 1) {
+    for (int u = 0; u < kStatTokens / 2; ++u) {
+        float x = dot8(o[u], od[u]);
+#pragma unroll
+        for (int m = 8; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+        x = __shfl_sync(0xffffffffu, x, (lane & 1) * 16);
+        if (lane >> 1 == u) mine = x;
+    }
+    const bool is_short = seen > 1 && seen <= kShortRow;
+    const uint32_t shorts = __ballot_sync(0xffffffffu, is_short);
+    if (real) {
+        stat[(long long)h * tokens + tok] = l == -INFINITY ? INFINITY : l * 1.44269504088896341f;
+        if (!is_short) stat[tokens * H + (long long)h * tokens + tok] = mine;
+    }
+    if (lane == 0) short_of[warp] = shorts;
+    if (is_short) {
+        const int i = warp * kStatTokens + lane;
+        short_k0[i] = k0;
+        short_keys[i] = (int)seen;
+        short_lse[i] = l;
+    }
+    __syncthreads();
+    // the block's short rows, dealt out to its warps (a sequence's first rows are all short)
+    unsigned long long todo = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) todo |= (unsigned long long)short_of[w] << (w * kStatTokens);
+    for (int turn = 0; todo; ++turn, todo &= todo - 1) {
+        if ((turn & 7) != warp) continue;
         // eight lanes to a key, four keys at a time, every load of the row on its way at once
-        const int i = __ffs(todo) - 1, W = kHeadDim + a.R, part = lane & 7;
-        const long long t = t0 + (i >> 4), first = __shfl_sync(0xffffffffu, k0, i);
-        const int cnt = (int)__shfl_sync(0xffffffffu, seen, i);
-        const float li = __shfl_sync(0xffffffffu, l, i);
+        const int i = __ffsll(todo) - 1, W = kHeadDim + a.R, part = lane & 7, cnt = short_keys[i];
+        const long long t = block0 + i, first = short_k0[i];
+        const float li = short_lse[i];
         const uint4 *q = reinterpret_cast<const uint4 *>(a.q + (t * H + h) * W), *d = reinterpret_cast<const uint4 *>(dout + (t * H + h) * kHeadDim);
         const uint4 q0 = q[part], q1 = q[8 + part], q2 = a.R ? q[16 + part] : make_uint4(0, 0, 0, 0), d0 = d[part], d1 = d[8 + part];
         float x[kShortRow / 4], dp[kShortRow / 4], sum = 0.f;
@@ -103,11 +137,7 @@ __global__ void __launch_bounds__(256) latent_stat_kernel(LatentArgs a, const __
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        if (lane == i) mine = sum;
-    }
-    if (real && (lane & 15) == 0) {
-        stat[(long long)h * tokens + tok] = l == -INFINITY ? INFINITY : l * 1.44269504088896341f;
-        stat[tokens * H + (long long)h * tokens + tok] = mine;
+        if (lane == 0) stat[tokens * H + (long long)h * tokens + t] = sum;
     }
 }
 
@@ -755,6 +785,7 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
 // float4 each per key.
 __global__ void __launch_bounds__(256) latent_dr_kernel(const float *__restrict__ dr_head, __nv_bfloat16 *__restrict__ dr, long long keys, int H)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");       // launched while the last blocks of dk and dq run
     const long long key = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int c = (threadIdx.x & 15) * 4;
     if (key >= keys) return;
@@ -790,7 +821,7 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
     const cudaError_t e = cudaFuncSetAttribute(latent_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return e;
     if (tokens > 0)
-        latent_stat_kernel<<<dim3((unsigned)((tokens + 15) / 16), a.H), 256, 0, stream>>>(a, b.dout, b.stat, tokens);
+        latent_stat_kernel<<<dim3((unsigned)((tokens + 8 * kStatTokens - 1) / (8 * kStatTokens)), a.H), 256, 0, stream>>>(a, b.dout, b.stat, tokens);
     // its blocks set up and load their first tiles while the statistics are being finished
     cudaLaunchAttribute at;
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -804,7 +835,16 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
     cfg.numAttrs = tokens > 0 ? 1 : 0;
     const cudaError_t e2 = cudaLaunchKernelEx(&cfg, latent_bwd_kernel, a, b, q_slots, k_slots, m);
     if (e2 != cudaSuccess) return e2;
-    if (a.R && keys > 0) latent_dr_kernel<<<(unsigned)((keys + 15) / 16), 256, 0, stream>>>(b.dr_head, b.dr, keys, a.H);
+    if (a.R && keys > 0) {
+        cudaLaunchConfig_t after = {};
+        after.gridDim = dim3((unsigned)((keys + 15) / 16));
+        after.blockDim = dim3(256);
+        after.stream = stream;
+        after.attrs = &at;
+        after.numAttrs = 1;
+        const cudaError_t e3 = cudaLaunchKernelEx(&after, latent_dr_kernel, (const float *)b.dr_head, b.dr, keys, a.H);
+        if (e3 != cudaSuccess) return e3;
+    }
     return cudaGetLastError();
 }
 
