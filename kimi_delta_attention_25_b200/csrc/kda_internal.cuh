@@ -235,6 +235,27 @@ struct BwdArgs {
 cudaError_t launch_chunk_bwd_scan(const BwdArgs &a, kda_dtype_t dtype, cudaStream_t stream);
 cudaError_t launch_chunk_bwd_local(const BwdArgs &a, kda_dtype_t dtype, cudaStream_t stream);
 
+// Launches a kernel whose blocks may be scheduled, and set themselves up, while the kernel before it in the stream ends.
+// Each of its threads executes griddepcontrol.wait before its first access to memory that the launch was given, which
+// returns when the kernel before is complete and its writes are visible. (No kernel of the call may end without: the
+// next one's wait is for its predecessor alone.) It takes 2 to 3 us off a call that follows another.
+template <typename T> struct Same { using type = T; };
+template <typename... P>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const typename Same<P>::type &...args)
+{
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Decode step (memory-bound state update in place), optionally with the layer's gate producers
 // and output norm.
 cudaError_t launch_decode(const void *q, const void *k, const void *v, const float *log_alpha,

@@ -47,6 +47,7 @@ static_assert(8 * kStatTokens <= 64, "a block's tokens, a bit each");
 __global__ void __launch_bounds__(256) latent_stat_kernel(LatentArgs a, const __nv_bfloat16 *__restrict__ dout, float *__restrict__ stat,
                                                           long long tokens)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && blockIdx.y == 0) check_call(a);
     __shared__ uint32_t short_of[8];           // bit = token of that warp that sees 2 to kShortRow keys
@@ -738,7 +739,10 @@ __global__ void __launch_bounds__(NT, 1)
 latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_slots, const __grid_constant__ BwdMaps maps)
 {
     extern __shared__ __align__(1024) unsigned char sm[];
-    if (blockIdx.x == 0 && a.T == 0) check_call(a);              // (else the statistics' kernel does)
+    if (a.T == 0) {                                               // (else the statistics' kernel does both)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (blockIdx.x == 0) check_call(a);
+    }
     const int h = blockIdx.x % a.H, warp = threadIdx.x >> 5;
     long long x = blockIdx.x / a.H;
     const bool keys = x < k_slots;
@@ -785,7 +789,7 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
 // float4 each per key.
 __global__ void __launch_bounds__(256) latent_dr_kernel(const float *__restrict__ dr_head, __nv_bfloat16 *__restrict__ dr, long long keys, int H)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");       // launched while the last blocks of dk and dq run
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long key = (long long)blockIdx.x * 16 + (threadIdx.x >> 4);
     const int c = (threadIdx.x & 15) * 4;
     if (key >= keys) return;
@@ -820,32 +824,16 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
         return cudaErrorNotSupported;
     const cudaError_t e = cudaFuncSetAttribute(latent_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return e;
+    cudaError_t err = cudaSuccess;
     if (tokens > 0)
-        latent_stat_kernel<<<dim3((unsigned)((tokens + 8 * kStatTokens - 1) / (8 * kStatTokens)), a.H), 256, 0, stream>>>(a, b.dout, b.stat, tokens);
+        err = launch_after(latent_stat_kernel, dim3((unsigned)((tokens + 8 * kStatTokens - 1) / (8 * kStatTokens)), a.H), 256, 0, stream,
+                           a, b.dout, b.stat, tokens);
     // its blocks set up and load their first tiles while the statistics are being finished
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((q_slots + k_slots) * a.H));
-    cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = SMEM;
-    cfg.stream = stream;
-    cfg.attrs = &at;
-    cfg.numAttrs = tokens > 0 ? 1 : 0;
-    const cudaError_t e2 = cudaLaunchKernelEx(&cfg, latent_bwd_kernel, a, b, q_slots, k_slots, m);
-    if (e2 != cudaSuccess) return e2;
-    if (a.R && keys > 0) {
-        cudaLaunchConfig_t after = {};
-        after.gridDim = dim3((unsigned)((keys + 15) / 16));
-        after.blockDim = dim3(256);
-        after.stream = stream;
-        after.attrs = &at;
-        after.numAttrs = 1;
-        const cudaError_t e3 = cudaLaunchKernelEx(&after, latent_dr_kernel, (const float *)b.dr_head, b.dr, keys, a.H);
-        if (e3 != cudaSuccess) return e3;
-    }
-    return cudaGetLastError();
+    if (err == cudaSuccess)
+        err = launch_after(latent_bwd_kernel, (unsigned)((q_slots + k_slots) * a.H), NT, SMEM, stream, a, b, q_slots, k_slots, m);
+    if (err == cudaSuccess && a.R && keys > 0)
+        err = launch_after(latent_dr_kernel, (unsigned)((keys + 15) / 16), 256, 0, stream, b.dr_head, b.dr, keys, a.H);
+    return err;
 }
 
 }  // namespace kda

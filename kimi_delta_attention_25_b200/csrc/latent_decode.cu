@@ -151,6 +151,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_c);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // The list of tiles: each thread counts a run of sequences, then finds whether this share begins in it.
     const int per = (a.N + NT - 1) / NT, n_lo = min(a.N, tid * per), n_hi = min(a.N, n_lo + per);
     bool bad = false;
@@ -715,23 +716,14 @@ cudaError_t launch(const DecodeArgs &a, const CUtensorMap &tq, const CUtensorMap
     auto kern = latent_decode_kernel<RG>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay<RG>::TOTAL);
     if (e != cudaSuccess) return e;
-    kern<<<a.L * a.G, Lay<RG>::NT, Lay<RG>::TOTAL, st>>>(a, tq, tc);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(kern, a.L * a.G, Lay<RG>::NT, Lay<RG>::TOTAL, st, a, tq, tc)) != cudaSuccess) return e;
     // the join's blocks may be scheduled while the last shares finish; they wait for the whole first kernel
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
     // at most one cut a share and one a sequence; with few of them a block per row and quarter, else four rows to a block
     const int by_share = 2 * a.N >= a.L, cuts = by_share ? a.L : a.N, rows = RG < a.Tq * a.H ? RG : a.Tq * a.H;
     const int rpb = cuts * a.G <= 8 ? 1 : 4;
-    cfg.gridDim = dim3(cuts * a.G, (rows + rpb - 1) / rpb, by_share ? 1 : 4);
-    cfg.blockDim = dim3(by_share ? 128 : 512);
-    cfg.stream = st;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    return by_share ? cudaLaunchKernelEx(&cfg, latent_decode_join<RG, 4>, a, rpb, by_share)
-                    : cudaLaunchKernelEx(&cfg, latent_decode_join<RG, 16>, a, rpb, by_share);
+    const dim3 grid(cuts * a.G, (rows + rpb - 1) / rpb, by_share ? 1 : 4);
+    return by_share ? launch_after(latent_decode_join<RG, 4>, grid, 128, 0, st, a, rpb, by_share)
+                    : launch_after(latent_decode_join<RG, 16>, grid, 512, 0, st, a, rpb, by_share);
 }
 
 }  // namespace

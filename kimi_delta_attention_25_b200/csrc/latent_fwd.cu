@@ -52,7 +52,6 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
     const uint32_t sbase = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.x % a.H;
-    if (blockIdx.x == 0) check_call(a);        // (other blocks set the status a second later at the earliest: a wait that ran out)
     // tensor memory and barriers, beside the search for the block's tile
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + OFF_BAR);
     volatile int *ctl = reinterpret_cast<volatile int *>(bars + N_BARS);      // [0] tensor memory, [1] abort
@@ -73,6 +72,8 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
         fence_mbar_init();
         if (a.Tk > 0) { tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_k); tma_prefetch_desc(&tm_v); }
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (blockIdx.x == 0) check_call(a);        // (other blocks set the status a second later at the earliest: a wait that ran out)
     LatentSpan span;
     long long r0;                              // the block's first row within its sequence
     bool some;
@@ -391,8 +392,7 @@ cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream)
         return cudaErrorNotSupported;
     const cudaError_t e = cudaFuncSetAttribute(latent_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return e;
-    latent_fwd_kernel<<<(unsigned)(slots * a.H), NT, SMEM, stream>>>(a, slots, tq, tk, tv, tr);
-    return cudaGetLastError();
+    return launch_after(latent_fwd_kernel, (unsigned)(slots * a.H), NT, SMEM, stream, a, slots, tq, tk, tv, tr);
 }
 
 }  // namespace kda

@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) rms_norm_kernel(NormPar
 {
     constexpr int NV = Vec<T>::n;
     __shared__ float red[TPR / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t = threadIdx.x % TPR;
     const long long row = (long long)blockIdx.x * (blockDim.x / TPR) + threadIdx.x / TPR;
     if (row >= p.rows) return;               // whole warps (TPR 32), or never (one row per block)
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float red[2][TPR / 32][2];
     __shared__ uint64_t full[kRowsAhead];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t = threadIdx.x, nvec = p.D / NV;
     const uint32_t row_bytes = (uint32_t)nvec * 16;
@@ -338,6 +340,7 @@ __global__ void __launch_bounds__(128) latent_append_kernel(const __nv_bfloat16 
                                                             __nv_bfloat16 *__restrict__ cache, long long c_stride,
                                                             long long r_stride, long long cache_rows, int T, int R, float eps)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (t >= T) return;
     const long long slot = slots[t];
@@ -378,17 +381,17 @@ __global__ void __launch_bounds__(128) latent_append_kernel(const __nv_bfloat16 
 bool al(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 template <typename T, bool RES, bool Q8>
-void launch_norm(const NormParams &p, cudaStream_t st)
+cudaError_t launch_norm(const NormParams &p, cudaStream_t st)
 {
     const int nvec = p.D / Vec<T>::n;
     auto go = [&](auto kern, int tpr) {
         const int threads = tpr > 128 ? tpr : 128, per = threads / tpr;
-        kern<<<(unsigned)((p.rows + per - 1) / per), threads, 0, st>>>(p);
+        return launch_after(kern, (unsigned)((p.rows + per - 1) / per), threads, 0, st, p);
     };
-    if (nvec <= 32 * 4) go(rms_norm_kernel<T, 32, 4, RES, Q8>, 32);
-    else if (nvec <= 128 * 4) go(rms_norm_kernel<T, 128, 4, RES, Q8>, 128);
-    else if (nvec <= 512 * 4) go(rms_norm_kernel<T, 512, 4, RES, Q8>, 512);
-    else go(rms_norm_kernel<T, 512, 8, RES, Q8>, 512);
+    if (nvec <= 32 * 4) return go(rms_norm_kernel<T, 32, 4, RES, Q8>, 32);
+    if (nvec <= 128 * 4) return go(rms_norm_kernel<T, 128, 4, RES, Q8>, 128);
+    if (nvec <= 512 * 4) return go(rms_norm_kernel<T, 512, 4, RES, Q8>, 512);
+    return go(rms_norm_kernel<T, 512, 8, RES, Q8>, 512);
 }
 
 kda_status_t run_norm(const void *x, const void *residual, const float *weight, void *y, float *scale, void *h,
@@ -406,14 +409,15 @@ kda_status_t run_norm(const void *x, const void *residual, const float *weight, 
     p.rows = rows; p.D = D;
     cudaStream_t st = (cudaStream_t)stream;
     using bf = __nv_bfloat16;
+    cudaError_t e;
     if (dtype == KDA_BF16) {
-        if (residual) q8 ? launch_norm<bf, true, true>(p, st) : launch_norm<bf, true, false>(p, st);
-        else q8 ? launch_norm<bf, false, true>(p, st) : launch_norm<bf, false, false>(p, st);
+        if (residual) e = q8 ? launch_norm<bf, true, true>(p, st) : launch_norm<bf, true, false>(p, st);
+        else e = q8 ? launch_norm<bf, false, true>(p, st) : launch_norm<bf, false, false>(p, st);
     } else {
-        if (residual) q8 ? launch_norm<float, true, true>(p, st) : launch_norm<float, true, false>(p, st);
-        else q8 ? launch_norm<float, false, true>(p, st) : launch_norm<float, false, false>(p, st);
+        if (residual) e = q8 ? launch_norm<float, true, true>(p, st) : launch_norm<float, true, false>(p, st);
+        else e = q8 ? launch_norm<float, false, true>(p, st) : launch_norm<float, false, false>(p, st);
     }
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 // Threads that hold a row of the backward pass, and its blocks: 1024 threads on each of 148 SMs.
@@ -437,8 +441,7 @@ cudaError_t launch_norm_bwd(const NormBwdParams &p, int blocks, cudaStream_t st)
             const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
             if (e != cudaSuccess) return e;
         }
-        kern<<<blocks, threads, ring, st>>>(p);
-        return cudaGetLastError();
+        return launch_after(kern, blocks, threads, ring, st, p);
     };
     if (nvec <= 32) return go(rms_norm_bwd_kernel<T, 32, 1, DH>, 32);
     if (nvec <= 128) return go(rms_norm_bwd_kernel<T, 128, 1, DH>, 128);
@@ -499,17 +502,7 @@ kda_status_t kda_rms_norm_bwd(const void *dy, const void *h, const float *weight
                                             : (dh ? launch_norm_bwd<float, true>(p, blocks, st) : launch_norm_bwd<float, false>(p, blocks, st));
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     // scheduled while the first kernel's last rows are worked on; it waits for all of them
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((D + 31) / 32);
-    cfg.blockDim = dim3(1024);
-    cfg.stream = st;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    const float *partial = p.partial;
-    return cudaLaunchKernelEx(&cfg, rms_norm_dw_kernel, partial, dweight, blocks, D) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    return launch_after(rms_norm_dw_kernel, (D + 31) / 32, 1024, 0, st, p.partial, dweight, blocks, D) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status_t kda_latent_append(const void *c, const void *k_shared, const long long *slots, const float *weight,
@@ -524,10 +517,10 @@ kda_status_t kda_latent_append(const void *c, const void *k_shared, const long l
     if (!al(c, 16) || !al(slots, 8) || !al(cache, 16) || !al(weight, 16)) return KDA_ERR_INVALID_ARG;
     if (c_token_stride % 8 != 0 || c_token_stride < 0) return KDA_ERR_INVALID_ARG;
     if (dr && (!al(k_shared, 16) || shared_token_stride % 8 != 0 || shared_token_stride < 0)) return KDA_ERR_INVALID_ARG;
-    latent_append_kernel<<<(T + 3) / 4, 128, 0, (cudaStream_t)stream>>>(
-        (const __nv_bfloat16 *)c, (const __nv_bfloat16 *)k_shared, slots, weight, (__nv_bfloat16 *)cache, c_token_stride,
-        shared_token_stride, cache_rows, T, dr, eps);
-    return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const cudaError_t e = launch_after(latent_append_kernel, (T + 3) / 4, 128, 0, (cudaStream_t)stream, (const __nv_bfloat16 *)c,
+                                       (const __nv_bfloat16 *)k_shared, slots, weight, (__nv_bfloat16 *)cache, c_token_stride,
+                                       shared_token_stride, cache_rows, T, dr, eps);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

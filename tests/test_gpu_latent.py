@@ -545,3 +545,53 @@ def test_layer_prompt_and_decode_together():
     size = want.square().mean().sqrt()
     assert float((absorbed - want).abs().max()) <= 2.0 ** -4 * 4 * float(size)
     assert float((absorbed - want).square().mean().sqrt()) <= 2.0 ** -5 * float(size)
+
+
+@pytest.mark.parametrize("N,H", [(3, 16), (40, 32)])
+def test_calls_that_read_one_anothers_results(N, H):
+    """A chain in which each call reads what the call before it wrote, without a pause: the same bits as with the
+    device idle between the calls, and as in a graph whose first nodes are a memset and copies."""
+    rows, page, D = N * H, 32, 576
+    g = torch.Generator().manual_seed(9)
+    x0 = torch.randn(rows, D, generator=g).to(B16).to(DEV)
+    w = (1 + 0.1 * torch.randn(D, generator=g)).to(DEV)
+    pages = -(-rows // page)
+    slots = torch.randperm(rows, generator=g).to(DEV)
+    table = torch.randint(0, pages, (N, 5), generator=g, dtype=torch.int32).to(DEV)
+    lens = torch.randint(1, 5 * page, (N,), generator=g, dtype=torch.int32).to(DEV)
+    x, cache = torch.empty_like(x0), torch.empty(pages, page, D, dtype=B16, device=DEV)
+
+    def chain(pause):
+        cache.zero_()
+        x.copy_(x0)
+        y, h, kept = x, x, []
+        for _ in range(4):
+            y, h = kda.rms_norm(y, w, residual=h)
+            pause()
+            kda.latent_append(y[:, :512], y[:, 512:], cache, slots)
+            pause()
+            o, _ = kda.latent_decode_step(y.view(N, 1, H, D), cache, table, lens)
+            pause()
+            q, kv = y.view(1, 3 * rows, 1, 192), o.view(1, 4 * rows, 1, 128)
+            k, v, r = kv[:, :3 * rows], kv[:, rows:], h.view(1, 9 * rows, 64)[:, :3 * rows]
+            out, lse = kda.latent_fwd(q, k, v, r)
+            pause()
+            grads = kda.latent_bwd(q, k, v, r, out, lse, out)
+            pause()
+            y, dw = kda.rms_norm_bwd(grads["dq"].view(rows, D), h, w, dh=grads["dk"].view(-1)[:rows * 128].repeat(5)[:rows * D].view(rows, D))
+            pause()
+            kept += [o, out, lse, grads["dk_shared"], grads["dv"], dw, y, kda.rms_norm_e4m3(out.view(-1, 128), w[:128])[1]]
+        return kept
+
+    want = [t.clone() for t in chain(torch.cuda.synchronize)]
+    assert all(bool(torch.isfinite(t.float()).all()) for t in want)
+    for _ in range(3):
+        for a, b in zip(chain(lambda: None), want):
+            assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(lambda: None)
+    for _ in range(3):
+        graph.replay()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
