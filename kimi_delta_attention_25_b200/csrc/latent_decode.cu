@@ -565,43 +565,51 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
 // Joins the partial results of each sequence that a cut runs through. Block (cut, rows of a group, quarter of
 // the channels) with `rpb` rows. A sequence with many parts takes the whole block to a row and quarter, each warp
 // adding every NW-th part; one with few parts takes a warp to a row, all of its channels, in the blocks of the
-// first quarter. The sums are added in a fixed order. The first block also gathers the blocks' errors into the
-// status word.
+// first quarter. The sums are added in a fixed order. One block more gathers the blocks' errors into the status word.
+// It is a chain of reads that depend on one another, each of them the way to L2 and back (the cut, the parts' maxima and
+// sums, the parts): what a read needs of the others is kept to that, and the first parts are on their way before
+// their factors are known.
 constexpr int kManyParts = 8;
-template <int RG, int NW>
-__global__ void __launch_bounds__(32 * NW) latent_decode_join(DecodeArgs a, int rpb, int by_share)
+template <int RG, int NW, int MINB>
+__global__ void __launch_bounds__(32 * NW, MINB) latent_decode_join(DecodeArgs a, int rpb, int by_share)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int cut = blockIdx.x / a.G, g = blockIdx.x % a.G, t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+    if (by_share ? blockIdx.x == gridDim.x - 1 : blockIdx.y == gridDim.y - 1) {       // the errors
+        if ((by_share ? blockIdx.y : blockIdx.x) || blockIdx.z) return;
         int err = 0;
         for (int i = t; i < a.L * a.G; i += 32 * NW) err = max(err, a.errs[i]);
         err = __syncthreads_or(err == KDA_ERR_TIMEOUT) ? KDA_ERR_TIMEOUT : (__syncthreads_or(err) ? KDA_ERR_INVALID_ARG : 0);
         if (t == 0) *a.status = err;
+        return;
     }
     // the share at whose end the cut-th cut sequence begins; with `by_share` (as many sequences as shares, or nearly)
     // block x looks at its own share instead of counting cuts
-    __shared__ int s_cut[NW], s_found;
+    __shared__ int s_cut[NW], s_found[3];
     __shared__ float4 s_o[NW][32];
-    int share = by_share ? cut : -1;
-    if (!by_share) {
+    int share = cut, n = -1, last = -1;
+    if (by_share) {
+        const int2 x = reinterpret_cast<const int2 *>(a.meta)[share];
+        n = x.x; last = x.y;
+    } else {
         int before = 0;
-        if (t == 0) s_found = -1;
+        if (t == 0) s_found[1] = -1;
         for (int base = 0; base < a.L; base += 32 * NW) {
             const int i = base + t;
-            const bool is = i < a.L && a.meta[2 * i] >= 0;
+            const int2 x = i < a.L ? reinterpret_cast<const int2 *>(a.meta)[i] : make_int2(-1, -1);
+            const bool is = x.x >= 0;
             const uint32_t ball = __ballot_sync(0xffffffffu, is);
             if (lane == 0) s_cut[warp] = __popc(ball);
             __syncthreads();
             int at = before + __popc(ball & ((1u << lane) - 1));
             for (int w = 0; w < NW; ++w) { if (w < warp) at += s_cut[w]; before += s_cut[w]; }
-            if (is && at == cut) s_found = i;
+            if (is && at == cut) { s_found[0] = i; s_found[1] = x.x; s_found[2] = x.y; }
             __syncthreads();
         }
-        share = s_found;
+        share = s_found[0]; n = s_found[1]; last = s_found[2];
     }
-    if (share < 0 || a.meta[2 * share] < 0) return;
-    const int n = a.meta[2 * share], last = a.meta[2 * share + 1], parts = last - share + 1;
+    if (n < 0) return;
+    const int parts = last - share + 1;
     const bool many = parts > kManyParts;
     if (!many && blockIdx.z > 0) return;
     const int quarters = 4 / gridDim.z;                        // of the channels, for this block, with many parts
@@ -639,7 +647,16 @@ __global__ void __launch_bounds__(32 * NW) latent_decode_join(DecodeArgs a, int 
     }
     constexpr int PT = (kLanes + 32 * NW - 1) / (32 * NW);     // parts of a thread
     __shared__ float s_f[kLanes], s_red[2][NW];
+    constexpr int EARLY = MINB == 1 ? 10 : 4;                                   // parts of a warp that are read before their factors are known
     for (int r = blockIdx.y * rpb; r < r_end; ++r) {
+        float4 x[EARLY];
+        auto part = [&](int s, int col) { return __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(s, r) * kLatentDim) + col); };
+        auto early = [&](int col) {
+#pragma unroll
+            for (int i = 0; i < EARLY; ++i)
+                if (warp + NW * i < parts) x[i] = part(warp + NW * i, col);
+        };
+        early(blockIdx.z * quarters * 32 + lane);
         float2 ml[PT];
         float m = -INFINITY, l = 0.f;
 #pragma unroll
@@ -669,11 +686,18 @@ __global__ void __launch_bounds__(32 * NW) latent_decode_join(DecodeArgs a, int 
         for (int qt = 0; qt < quarters; ++qt) {
             const int col = (blockIdx.z * quarters + qt) * 32 + lane;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 10
-            for (int s = warp; s < parts; s += NW) {
+            if (qt > 0) early(col);
+#pragma unroll
+            for (int i = 0; i < EARLY; ++i)
+                if (warp + NW * i < parts) {
+                    const float f = s_f[warp + NW * i];
+                    o.x += f * x[i].x; o.y += f * x[i].y; o.z += f * x[i].z; o.w += f * x[i].w;
+                }
+#pragma unroll 4
+            for (int s = warp + NW * EARLY; s < parts; s += NW) {
                 const float f = s_f[s];
-                const float4 x = __ldcs(reinterpret_cast<const float4 *>(a.part + slot_of(s, r) * kLatentDim) + col);
-                o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+                const float4 y = part(s, col);
+                o.x += f * y.x; o.y += f * y.y; o.z += f * y.z; o.w += f * y.w;
             }
             s_o[warp][lane] = o;
             __syncthreads();
@@ -721,9 +745,12 @@ cudaError_t launch(const DecodeArgs &a, const CUtensorMap &tq, const CUtensorMap
     // at most one cut a share and one a sequence; with few of them a block per row and quarter, else four rows to a block
     const int by_share = 2 * a.N >= a.L, cuts = by_share ? a.L : a.N, rows = RG < a.Tq * a.H ? RG : a.Tq * a.H;
     const int rpb = cuts * a.G <= 8 ? 1 : 4;
-    const dim3 grid(cuts * a.G, (rows + rpb - 1) / rpb, by_share ? 1 : 4);
-    return by_share ? launch_after(latent_decode_join<RG, 4>, grid, 128, 0, st, a, rpb, by_share)
-                    : launch_after(latent_decode_join<RG, 16>, grid, 512, 0, st, a, rpb, by_share);
+    const dim3 grid(cuts * a.G + (by_share ? 1 : 0), (rows + rpb - 1) / rpb + (by_share ? 0 : 1), by_share ? 1 : 4);
+    // with a block to an SM at most, ten parts a warp are read early (one sequence of 128K tokens, 32 heads: 43.2 us with
+    // none, 40.3 so); with more blocks, four, so that two fit
+    if (by_share) return launch_after(latent_decode_join<RG, 4, 8>, grid, 128, 0, st, a, rpb, by_share);
+    if (cuts * a.G * ((rows + rpb - 1) / rpb) * 4 <= kLanes) return launch_after(latent_decode_join<RG, 16, 1>, grid, 512, 0, st, a, rpb, by_share);
+    return launch_after(latent_decode_join<RG, 16, 2>, grid, 512, 0, st, a, rpb, by_share);
 }
 
 }  // namespace

@@ -208,38 +208,45 @@ def latent_append(c, k_shared, cache, slots, weight=None, eps=1e-5):
     c [T,512] and k_shared [T,dr] or None, bf16 (rows with a stride allowed), cache [pages,page_size,512+dr]
     bf16 (updated in place and returned), slots int64 [T] (rows of the flattened cache, each at most once;
     rows outside it, such as -1, are skipped). ``weight`` fp32 [512], or None for c as it is."""
-    if c.dim() != 2 or cache.dim() != 3:
+    shape, rows = c.shape, cache.shape
+    if len(shape) != 2 or len(rows) != 3:
         raise ValueError("c must be [T, 512] and cache [pages, page_size, D]")
     dev = c.get_device()
-    T, dr = c.shape[0], 0 if k_shared is None else k_shared.shape[-1]
+    (T, dc), (pages, page, _) = shape, rows
+    dr = 0 if k_shared is None else k_shared.shape[-1]
     _check("c", c, _BF16, dev, dense=False)
-    _check("cache", cache, _BF16, dev, (*cache.shape[:2], c.shape[1] + dr))
+    _check("cache", cache, _BF16, dev, (pages, page, dc + dr))
     _check("slots", slots, _I64, dev, (T,))
+    cs, step = c.stride()
+    rs, step_r = 0, 1
     if k_shared is not None:
         _check("k_shared", k_shared, _BF16, dev, (T, dr), dense=False)
+        if dr:
+            rs, step_r = k_shared.stride()
     if weight is not None:
-        _check("weight", weight, _F32, dev, (c.shape[1],))
-    if c.stride(1) != 1 or (dr and k_shared.stride(1) != 1):
+        _check("weight", weight, _F32, dev, (dc,))
+    if step != 1 or step_r != 1:
         raise ValueError("the channels of c and k_shared must be contiguous")
-    cs, rs = (c.stride(0) if T > 1 else 0), (k_shared.stride(0) if dr and T > 1 else 0)
-    _call("kda_latent_append", dev, (_p(c), _p(k_shared), _p(slots), _p(weight), _p(cache), cs, rs,
-                                     cache.shape[0] * cache.shape[1], T, c.shape[1], dr, eps, _kda.KDA_BF16))
+    if T <= 1:
+        cs = rs = 0                       # a stride that is never used
+    _call("kda_latent_append", dev, (_p(c), _p(k_shared), _p(slots), _p(weight), _p(cache), cs, rs, pages * page, T, dc, dr,
+                                     eps, _kda.KDA_BF16))
     return cache
 
 
 def _norm_args(x, weight, residual, residual_out):
-    dev = x.get_device()
-    D = x.shape[-1]
-    if x.dtype not in (_F32, _BF16):
-        raise TypeError("x must be float32 or bfloat16, got %s" % x.dtype)
-    _check("x", x, x.dtype, dev)
+    dev, dtype, shape = x.get_device(), x.dtype, x.shape
+    D = shape[-1]
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError("x must be float32 or bfloat16, got %s" % dtype)
+    _check("x", x, dtype, dev)
     _check("weight", weight, _F32, dev, (D,))
     if residual is None:
         return dev, D, x
-    _check("residual", residual, x.dtype, dev, x.shape)
+    _check("residual", residual, dtype, dev, shape)
     if residual_out is None:
         return dev, D, torch.empty_like(x)
-    _check("residual_out", residual_out, x.dtype, dev, x.shape)
+    _check("residual_out", residual_out, dtype, dev, shape)
     return dev, D, residual_out
 
 
