@@ -61,9 +61,8 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows(name, t):
-    """Token and head strides of a [B, Tk, H, 128] view whose batch rows follow one another."""
-    B, L, H, D = t.shape
+def _rows(name, t, B, L, H, D):
+    """Token and head strides of a [B, L, H, D] view whose batch rows follow one another."""
     sb, st, sh, sc = t.stride()
     if sc != 1 or (B > 1 and sb != L * st):
         raise ValueError("%s: channels must be contiguous and batch rows follow one another" % name)
@@ -73,16 +72,17 @@ def _rows(name, t):
 
 def _expanded(q, k, v, k_shared, cu_q, cu_k):
     """Checks of the expanded form's inputs; sizes and strides as the C call takes them."""
-    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+    shape, k_shape, v_shape = q.shape, k.shape, v.shape
+    if len(shape) != 4 or len(k_shape) != 4 or len(v_shape) != 4:
         raise ValueError("q, k and v must be [B, T, H, D]")
     dev = q.get_device()
-    B, T, H, W = q.shape
-    Tk = k.shape[1]
+    B, T, H, _ = shape
+    Tk, dk, dv = k_shape[1], k_shape[3], v_shape[3]
     dr = 0 if k_shared is None else k_shared.shape[-1]
-    _check("q", q, _BF16, dev, (B, T, H, k.shape[-1] + dr))
-    _check("k", k, _BF16, dev, (B, Tk, H, k.shape[-1]), dense=False)
-    _check("v", v, _BF16, dev, (B, Tk, H, v.shape[-1]), dense=False)
-    ks, vs, rs = _rows("k", k), _rows("v", v), 0
+    _check("q", q, _BF16, dev, (B, T, H, dk + dr))
+    _check("k", k, _BF16, dev, (B, Tk, H, dk), dense=False)
+    _check("v", v, _BF16, dev, (B, Tk, H, dv), dense=False)
+    ks, vs, rs = _rows("k", k, B, Tk, H, dk), _rows("v", v, B, Tk, H, dv), 0
     if k_shared is not None:
         _check("k_shared", k_shared, _BF16, dev, (B, Tk, dr), dense=False)
         sb, rs, sc = k_shared.stride()
@@ -95,8 +95,9 @@ def _expanded(q, k, v, k_shared, cu_q, cu_k):
     if cu_q is not None:
         N = cu_q.shape[0] - 1
         _check("cu_seqlens", cu_q, _I32, dev, (N + 1,))
-        _check("cu_seqlens_k", cu_k, _I32, dev, (N + 1,))
-    return dev, (B, T, Tk, H, N, k.shape[-1], v.shape[-1], dr), (*ks, *vs, rs)
+        if cu_k is not cu_q:
+            _check("cu_seqlens_k", cu_k, _I32, dev, (N + 1,))
+    return dev, (B, T, Tk, H, N, dk, dv, dr), (*ks, *vs, rs)
 
 
 def _workspace(workspace, size, like):
@@ -149,15 +150,14 @@ def latent_bwd(q, k, v, k_shared, out, lse, dout, cu_seqlens=None, cu_seqlens_k=
     _check("out", out, _BF16, dev, (B, T, H, dv))
     _check("lse", lse, _F32, dev, (B, T, H))
     _check("dout", dout, _BF16, dev, (B, T, H, dv))
-    shapes = {"dq": q.shape, "dk": (B, Tk, H, dk), "dv": (B, Tk, H, dv), "dk_shared": (B, Tk, dr) if dr else None}
     g = dict(grads) if grads is not None else {}
-    for key, shape in shapes.items():
-        if shape is None:
+    for key, like in (("dq", q), ("dk", k), ("dv", v), ("dk_shared", k_shared if dr else None)):
+        if like is None:
             g[key] = None
         elif g.get(key) is None:
-            g[key] = q.new_empty(shape)
+            g[key] = torch.empty_like(like, memory_format=torch.contiguous_format)
         else:
-            _check(key, g[key], _BF16, dev, shape)
+            _check(key, g[key], _BF16, dev, like.shape)
     ws = _workspace(workspace, latent_bwd_workspace_size(B, T, Tk, H, N, dr), q)
     _call("kda_latent_bwd", dev, (_p(q), _p(k), _p(v), _p(k_shared), _p(cu_seqlens), _p(cu_seqlens_k), _p(out), _p(lse),
                                   _p(dout), _p(g["dq"]), _p(g["dk"]), _p(g["dv"]), _p(g["dk_shared"]), *dims, *strides,
