@@ -21,7 +21,7 @@ namespace {
 using namespace sm100;
 
 constexpr int TL = 128;                       // rows and columns of a tile
-constexpr int NT = 8 * 32 + 96, W_LOAD = 8, W_MMA = 9;   // two issuing warps (one takes longer than the tensor cores)
+constexpr int NT = 8 * 32 + 96, W_LOAD = 8, W_MMA = 9;   // warp 10: dq issues its accumulation there, dk and dv fetch statistics
 constexpr uint32_t UNIT = 16384;              // 128 rows x 64 channels, 128-byte swizzle
 constexpr uint32_t SMEM_MAX = 232448;
 
