@@ -439,7 +439,7 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, const LatentBwdArg
 constexpr uint32_t K_A1 = 0, K_A2 = 3 * UNIT, K_B1 = 5 * UNIT, K_B2 = K_B1 + 6 * UNIT, K_STAT = 14 * UNIT;
 static_assert(K_B2 + 2 * UNIT <= K_STAT && K_STAT + 2048 <= OFF_BAR, "shared memory");
 enum { K_RES, K_F1, K_E1 = K_F1 + 2, K_F2 = K_E1 + 2, K_E2, K_S, K_P, K_PREADY, K_DS, K_DR, K_PFREE, K_ACC, K_STATF,
-       K_DRAIN = K_STATF + 2, K_NBARS };
+       K_STATE = K_STATF + 2, K_DRAIN = K_STATE + 2, K_NBARS };
 static_assert((int)K_NBARS <= kMaxBars, "barriers");
 constexpr uint32_t TK_S = 0, TK_P = 128, TK_DR = TK_P + 32, TK_DK = 256, TK_DV = 384;
 
@@ -580,7 +580,9 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, const LatentBwdAr
                 x[e] = c < Lq ? lse[c] : 0.f;
                 y[e] = c < Lq ? d[c] : 0.f;
             }
-            if (j >= 2) { wait(K_DS, j & 1); __syncwarp(); }
+            // The buffer's own barrier (one that completes every tile would not do: the warps may be done with tile j - 1
+            // before this one looks for tile j - 2, and the parities are the same again)
+            if (j >= 2) { wait(K_STATE + (j & 1), ((j >> 1) - 1) & 1); __syncwarp(); }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float *to = stat + (j & 1) * 256 + (e >> 1) * 128 + (e & 1) * 32 + lane;
@@ -700,7 +702,7 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, const LatentBwdAr
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[K_DS]);
+            if (lane == 0) { mbar_arrive(&bars[K_DS]); mbar_arrive(&bars[K_STATE + (j & 1)]); }
         }
         if (nt > 0) {
             if (has_r) take_dr(nt - 1);
@@ -755,7 +757,7 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
     if (warp == W_MMA) { tmem_alloc(const_cast<uint32_t *>(reinterpret_cast<volatile uint32_t *>(ctl)), 512); tmem_relinquish(); }
     if (warp == W_LOAD && elect_one()) {
         for (int i = 0; i < (keys ? (int)K_NBARS : (int)G_NBARS); ++i) {
-            const bool by_warps = keys ? i == K_PREADY || i == K_DS || i == K_PFREE : i == G_SFREE || i == G_PFREE || i == G_DS;
+            const bool by_warps = keys ? i == K_PREADY || i == K_DS || i == K_PFREE || i == K_STATE || i == K_STATE + 1 : i == G_SFREE || i == G_PFREE || i == G_DS;
             mbar_init(&bars[i], by_warps ? 8 : 1);
         }
         ctl[1] = 0;

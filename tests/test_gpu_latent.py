@@ -203,6 +203,21 @@ def test_expanded_empty_sizes():
     assert all(torch.all(g[x] == 0) for x in ("dk", "dv", "dk_shared"))
 
 
+@pytest.mark.parametrize("R", [64, 0])
+def test_expanded_backward_over_many_query_tiles(R):
+    """Blocks of dk and dv that walk twelve tiles of queries, whose statistics go through two buffers in turn."""
+    lens_q, lens_k = [1500], [70]
+    q, k, v, r, dout = expanded(lens_q, lens_k, 2, R, seed=31)
+    cu = (cu_of(lens_q), cu_of(lens_k))
+    for causal in (True, False):
+        out, lse = kda.latent_fwd(q, k, v, r, *cu, causal=causal)
+        ro = check_forward(q, k, v, r, lens_q, lens_k, causal, out, lse)
+        out = torch.tensor(ro, dtype=torch.float32, device=DEV).to(B16)[None]
+        g, ws = kda.latent_bwd(q, k, v, r, out, lse, dout, *cu, causal=causal, return_workspace=True)
+        assert kda.workspace_status(ws) == kda.KDA_OK
+        check_backward(q, k, v, r, dout, lens_q, lens_k, causal, g)
+
+
 def test_expanded_gradients_of_short_rows():
     """Rows that see one key have no gradient through the softmax (exactly), and those that see a few keep their
     accuracy although ``out`` was rounded: over all rows two roundings to bf16, each at most 2^-8 of a value and of
