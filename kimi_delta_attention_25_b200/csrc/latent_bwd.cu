@@ -345,7 +345,6 @@ __device__ __forceinline__ void dq_block(const LatentArgs &a, const LatentBwdArg
         const float sc = a.scale * 1.44269504088896341f;
         const long long tokens = (long long)a.B * a.T;
         const float *st_lse = b.stat + (size_t)h * tokens, *st_d = st_lse + (size_t)tokens * a.H;
-        asm volatile("griddepcontrol.wait;" ::: "memory");   // the statistics' kernel, whose end this block may overlap
         float lse_r = 0.f, d_r = 0.f;
         if (real) { lse_r = st_lse[row_first + row]; d_r = st_d[row_first + row]; }
         // keys this row sees (a query that sees one key has P = 1 whatever its score: dS is 0, which dP - D would miss
@@ -568,7 +567,6 @@ __device__ __forceinline__ void dkv_block(const LatentArgs &a, const LatentBwdAr
         }
     } else if (warp == W_MMA + 1) {
         // ====================================================== the columns' statistics, [buffer][group][lse, D][64]
-        asm volatile("griddepcontrol.wait;" ::: "memory");   // their kernel, whose end this block may overlap
         const long long tokens = (long long)a.B * a.T;
         const float *lse = b.stat + (size_t)h * tokens + sp.q0, *d = lse + (size_t)tokens * a.H;
         float *stat = reinterpret_cast<float *>(sm + K_STAT);
@@ -743,10 +741,6 @@ __global__ void __launch_bounds__(NT, 1)
 latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_slots, const __grid_constant__ BwdMaps maps)
 {
     extern __shared__ __align__(1024) unsigned char sm[];
-    if (a.T == 0) {                                               // (else the statistics' kernel does both)
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (blockIdx.x == 0) check_call(a);
-    }
     const int h = blockIdx.x % a.H, warp = threadIdx.x >> 5;
     long long x = blockIdx.x / a.H;
     const bool keys = x < k_slots;
@@ -764,6 +758,10 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
         fence_mbar_init();
         if (a.T > 0 && a.Tk > 0) { tma_prefetch_desc(&maps.q); tma_prefetch_desc(&maps.k); tma_prefetch_desc(&maps.v); tma_prefetch_desc(&maps.d); }
     }
+    // Inputs, offsets and statistics alike are read behind this wait only: that the statistics' kernel has waited for what
+    // was before it makes those writes visible to its own threads, not to a kernel that overlaps it.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.T == 0 && blockIdx.x == 0) check_call(a);               // (else the statistics' kernel does it)
     LatentSpan sp;
     long long r0;
     int n;
@@ -776,13 +774,9 @@ latent_bwd_kernel(LatentArgs a, LatentBwdArgs b, long long q_slots, long long k_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(ctl);
-    if (!some) {
-        // no block ends before the statistics' kernel has: what follows this kernel must not overtake that one
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-    } else if (keys) {
-        dkv_block(a, b, sp, r0, h, maps, sm);
-    } else {
-        dq_block(a, b, sp, r0, h, maps, sm);
+    if (some) {
+        if (keys) dkv_block(a, b, sp, r0, h, maps, sm);
+        else dq_block(a, b, sp, r0, h, maps, sm);
     }
     tc_fence_before();
     __syncthreads();
@@ -832,7 +826,7 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
     cudaError_t err = cudaSuccess;
     if (tokens > 0)
         err = launch_after(latent_stat_kernel, (unsigned)stat_blocks, 256, 0, stream, a, b.dout, b.stat, tokens);
-    // its blocks set up and load their first tiles while the statistics are being finished
+    // its blocks set themselves up while the statistics are being finished
     if (err == cudaSuccess)
         err = launch_after(latent_bwd_kernel, (unsigned)((q_slots + k_slots) * a.H), NT, SMEM, stream, a, b, q_slots, k_slots, m);
     if (err == cudaSuccess && a.R && keys > 0)
