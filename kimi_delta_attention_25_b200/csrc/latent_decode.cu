@@ -148,8 +148,7 @@ latent_decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap tm_q, con
         mbar_init(&bars[B_DRAIN], 1);
         ctl[1] = 0; ctl[2] = 0; ctl[3] = a.N; ctl[4] = 0; ctl[5] = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_c);
+        if (a.pages > 0) { tma_prefetch_desc(&tm_q); tma_prefetch_desc(&tm_c); }     // (else they were not made)
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // The list of tiles: each thread counts a run of sequences, then finds whether this share begins in it.

@@ -388,6 +388,17 @@ def test_absorbed_bad_lengths_and_pages_are_reported():
         assert torch.equal(out[0], want[0][0]) and torch.equal(out[2], want[0][2])
 
 
+@pytest.mark.parametrize("width", [0, 3])
+def test_absorbed_empty_cache(width):
+    """A cache without a page: idle slots get zeros, a length above zero is reported."""
+    q = torch.randn(3, 1, 8, 576, device=DEV).to(B16)
+    cache, table = torch.empty(0, 64, 576, dtype=B16, device=DEV), torch.zeros(3, width, dtype=torch.int32, device=DEV)
+    for lens, status in (([0, 0, 0], kda.KDA_OK), ([0, 5, 0], kda.KDA_ERR_INVALID_ARG)):
+        out, lse, ws = kda.latent_decode_step(q, cache, table, torch.tensor(lens, dtype=torch.int32, device=DEV), return_workspace=True)
+        assert kda.workspace_status(ws) == status
+        assert torch.all(out == 0) and torch.all(lse == -float("inf"))
+
+
 def test_absorbed_streams_graphs_and_two_workspaces():
     a, b = paged([500, 77], 16, 64, 1, 64, seed=1), paged([90, 333], 16, 64, 1, 64, seed=2)
     wa, wb = kda.latent_decode_step(*a), kda.latent_decode_step(*b)
