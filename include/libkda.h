@@ -491,7 +491,8 @@ kda_status_t kda_rms_norm_e4m3(const void *x, const void *residual, const float 
 /* Its backward pass: dx = the gradient through the norm at h, plus dh (the gradient that reaches h along
  * the residual stream; NULL: none): the gradient of x and of the residual alike. dweight fp32 [D]
  * (written; zeros for rows = 0). dy, h, dh, dx [rows, D] dtype; dx may alias dy, h or dh. No atomic sums.
- * Workspace: kda_rms_norm_bwd_workspace_size(rows, D) bytes, 16-byte aligned (no status word). */
+ * Workspace: kda_rms_norm_bwd_workspace_size(rows, D) bytes, 16-byte aligned (no status word: a device-side wait that gave
+ * up leaves NaN in all of dweight and in the rows of dx that it concerns). */
 size_t kda_rms_norm_bwd_workspace_size(long long rows, int D);
 kda_status_t kda_rms_norm_bwd(const void *dy, const void *h, const float *weight, const void *dh, void *dx,
                               float *dweight, long long rows, int D, float eps, kda_dtype_t dtype,

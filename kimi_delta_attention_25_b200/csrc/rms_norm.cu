@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float red[2][TPR / 32][2];
     __shared__ uint64_t full[kRowsAhead];
+    __shared__ int stop;                     // a wait ran out (1), and the copies in flight have been waited for (2)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int t = threadIdx.x, nvec = p.D / NV;
@@ -223,6 +224,7 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
     if constexpr (AHEAD) {
         if (t == 0) {
             for (int s = 0; s < kRowsAhead; ++s) sm100::mbar_init(&full[s], 1);
+            stop = 0;
             sm100::fence_mbar_init();
         }
         __syncthreads();
@@ -230,14 +232,25 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
             for (int s = 0; s < kRowsAhead; ++s) order(blockIdx.x + (long long)s * gridDim.x, s);
         weights(t, w1);
     }
+    // A wait that runs out (the call has no status word to record it in): from that row on this thread's sum is NaN, and with
+    // it the block's rows of dx and all of dweight. The other waits then give up at once, no copy is ordered any more, and
+    // what is in flight lands before the block ends.
+    bool stopped = false;
+    auto arrived = [&](int s, uint32_t parity) {
+        if (sm100::mbar_try_wait(&full[s], parity)) return true;
+        const long long t0 = clock64();
+        while (!sm100::mbar_try_wait(&full[s], parity)) {
+            if (*(volatile int *)&stop) return false;
+            if (clock64() - t0 > 4000000000LL) { *(volatile int *)&stop = 1; return false; }
+        }
+        return true;
+    };
     int it = 0;
     for (long long row = blockIdx.x; row < p.rows; row += gridDim.x, ++it) {
         const int flip = it & 1, stage = it % kRowsAhead;
         uint4 hv[VPT], gv[VPT], ev = make_uint4(0, 0, 0, 0);
         if constexpr (AHEAD) {
-            // (a copy that did not come within two seconds leaves what the stage holds: a device fault, which the
-            // next call reports)
-            sm100::mbar_wait(&full[stage], (it / kRowsAhead) & 1);
+            stopped = stopped || !arrived(stage, (it / kRowsAhead) & 1);
             const uint4 *src = reinterpret_cast<const uint4 *>(ring + (size_t)stage * (DH ? 3 : 2) * row_bytes);
             hv[0] = gv[0] = make_uint4(0, 0, 0, 0);
             if (t < nvec) {
@@ -249,7 +262,7 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) { hv[i] = fetch(p.h, row, i * TPR + t); gv[i] = fetch(p.dy, row, i * TPR + t); }
         }
-        float ss = 0.f, sg = 0.f;
+        float ss = AHEAD && stopped ? __int_as_float(0x7fc00000) : 0.f, sg = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             float h[NV], g[NV], wl[NV];
@@ -276,7 +289,14 @@ __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
             __syncwarp();
         }
         if constexpr (AHEAD)
-            if (t == 0) order(row + (long long)kRowsAhead * gridDim.x, stage);
+            if (t == 0) {
+                if (!stopped) order(row + (long long)kRowsAhead * gridDim.x, stage);
+                else if (*(volatile int *)&stop != 2) {
+                    for (int i = it; i < it + kRowsAhead; ++i)
+                        (void)sm100::mbar_wait(&full[i % kRowsAhead], (i / kRowsAhead) & 1, 100000000LL);
+                    *(volatile int *)&stop = 2;
+                }
+            }
         if constexpr (TPR > 32) {
             ss = red[flip][0][0];
             sg = red[flip][0][1];

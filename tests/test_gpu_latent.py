@@ -455,6 +455,34 @@ def test_rms_norm(rows, D, dtype):
         assert np.all(np.abs(f64(dw) - rw) <= (rel * 2 + (rows + 8) * 2.0 ** -24) * wide + 1e-30)
 
 
+@pytest.mark.parametrize("rows,D,dtype", [
+    (20003, 128, "bf16"), (6001, 1000, "bf16"), (3001, 2048, "bf16"), (1531, 4096, "bf16"), (743, 8192, "bf16"), (743, 4096, "f32"),
+    (1501, 4104, "f32"), (1501, 10000, "bf16"), (650, 16384, "f32")])
+def test_rms_norm_backward_of_many_rows(rows, D, dtype):
+    """More rows than blocks: each block walks several, the last of them not all as many, for every number of threads
+    that holds a row; bounds as in ``test_rms_norm``."""
+    dt, half = (B16, HALF) if dtype == "bf16" else (torch.float32, 0.0)
+    g = torch.Generator().manual_seed(rows)
+    h, dy, dh = (torch.randn(rows, D, generator=g).to(dt).to(DEV) for _ in range(3))
+    w = (1 + 0.1 * torch.randn(D, generator=g)).to(DEV)
+    rel = (D / 2 + 8) * 2.0 ** -24
+    rx, rw, wide = O.rms_norm_backward(f64(dy), f64(h), f64(w), 1e-5)
+    hh, gg = f64(h), np.abs(f64(dy) * f64(w))
+    rms = np.sqrt((hh * hh).mean(-1, keepdims=True) + 1e-5)
+    size = gg / rms + np.abs(hh) / rms ** 3 * (gg * np.abs(hh)).mean(-1, keepdims=True)
+    for extra in (None, dh):
+        dx, dw = kda.rms_norm_bwd(dy, h, w, dh=extra)
+        ad = 0.0 if extra is None else f64(extra)
+        assert np.all(np.abs(f64(dx) - rx - ad) <= half * np.abs(rx + ad) + (3 * rel * size + 2.0 ** -23 * np.abs(ad)) * (1 + half) + 1e-30)
+        assert np.all(np.abs(f64(dw) - rw) <= (rel * 2 + (rows + 8) * 2.0 ** -24) * wide + 1e-30)
+    # in place over each of its inputs
+    want = kda.rms_norm_bwd(dy, h, w, dh=dh)
+    for over in range(3):
+        a = [t.clone() for t in (dy, h, dh)]
+        got = kda.rms_norm_bwd(a[0], a[1], w, dh=a[2], dx=a[over])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,D", [(1, 128), (37, 256), (5, 1152), (3, 4096), (2, 16384)])
 def test_rms_norm_e4m3(rows, D, dtype):

@@ -10,8 +10,7 @@ import os
 import pytest
 
 WARPS = 2
-SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kimi_delta_attention_25_b200", "csrc",
-                      "latent_bwd.cu")
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "kimi_delta_attention_25_b200", "csrc")
 
 
 class Block:
@@ -140,7 +139,7 @@ def dq_block(tiles):
 @pytest.mark.parametrize("shared", [True, False])
 @pytest.mark.parametrize("tiles", [1, 2, 5])
 def test_dk_and_dv_blocks_never_wait_for_a_phase_that_is_past(tiles, shared):
-    with open(SOURCE) as f:
+    with open(os.path.join(CSRC, "latent_bwd.cu")) as f:
         own = "wait(K_STATE + (j & 1), ((j >> 1) - 1) & 1)" in f.read()          # which of the two the kernel does
     assert dkv_block(tiles, shared, own).search() is None
 
@@ -153,3 +152,11 @@ def test_one_barrier_for_both_statistics_buffers_can_be_overtaken():
 @pytest.mark.parametrize("tiles", [1, 2, 4])
 def test_dq_blocks_never_wait_for_a_phase_that_is_past(tiles):
     assert dq_block(tiles).search() is None
+
+
+def test_no_wait_of_the_norms_runs_out_unnoticed():
+    """The norm's calls have no status word, so a wait that gave up must show in the results: the outcome of every
+    bounded wait is used (or dropped in so many words, where copies in flight are waited for after that)."""
+    with open(os.path.join(CSRC, "rms_norm.cu")) as f:
+        lines = [x.strip() for x in f if "mbar_wait(" in x]
+    assert lines and not [x for x in lines if x.startswith(("mbar_wait(", "sm100::mbar_wait("))]
