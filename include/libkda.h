@@ -399,7 +399,8 @@ kda_status_t kda_chunk_fwd_noalloc_status(void *stream, int32_t *status);
  *   cu_seqlens, cu_seqlens_k  both NULL: N = B, batch row b has T queries and Tk keys. Otherwise int32
  *              [N+1] device arrays of packed offsets of the queries and of the keys (B = 1): first 0,
  *              non-decreasing, last T (Tk). A violation writes KDA_ERR_INVALID_ARG to the workspace
- *              status word; sequences whose offsets lie outside the tensors are skipped.
+ *              status word; sequences whose offsets lie outside the tensors are skipped. (N = 0 with
+ *              queries or keys returns KDA_ERR_INVALID_ARG.)
  *   causal     nonzero: query i of a sequence with Lq queries and Lk keys sees the keys
  *              j <= i + Lk - Lq (its last query sees every key: new tokens behind a history).
  *              Zero: every key of its sequence.

@@ -138,6 +138,8 @@ kda_status_t check_latent(const void *q, const void *k, const void *v, const voi
                           size_t need, LatentArgs *a);
 
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream);
+// A call without work: its status word, cleared or with what the offsets break.
+cudaError_t launch_latent_check(const LatentArgs &a, cudaStream_t stream);
 
 struct LatentBwdArgs {
     const __nv_bfloat16 *dout;

@@ -873,8 +873,8 @@ kda_status_t kda_latent_bwd(const void *q, const void *k, const void *v, const v
     b.stat = (float *)((unsigned char *)workspace + kStatusBytes);
     b.dr_head = (float *)((unsigned char *)b.stat + align256((size_t)B * T * H * 8));
     cudaStream_t st = (cudaStream_t)stream;
-    if (N == 0 || B == 0 || (T == 0 && Tk == 0)) return cudaMemsetAsync(workspace, 0, kStatusBytes, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
-    return launch_latent_bwd(a, b, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const cudaError_t e = N == 0 || B == 0 || (T == 0 && Tk == 0) ? launch_latent_check(a, st) : launch_latent_bwd(a, b, st);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

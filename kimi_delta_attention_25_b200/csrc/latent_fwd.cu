@@ -345,6 +345,12 @@ latent_fwd_kernel(LatentArgs a, long long slots, const __grid_constant__ CUtenso
     if (warp == W_MMA) tmem_dealloc(tmem, 512);
 }
 
+__global__ void __launch_bounds__(256) latent_check_kernel(LatentArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    check_call(a);
+}
+
 bool al(const void *p, size_t n) { return ((uintptr_t)p % n) == 0; }
 
 }  // namespace
@@ -359,6 +365,7 @@ kda_status_t check_latent(const void *q, const void *k, const void *v, const voi
     if (B < 0 || T < 0 || Tk < 0 || N < 0 || H <= 0) return KDA_ERR_INVALID_ARG;
     if ((cu_q == nullptr) != (cu_k == nullptr)) return KDA_ERR_INVALID_ARG;
     if (cu_q ? (B != 1 || !al(cu_q, 4) || !al(cu_k, 4)) : N != B) return KDA_ERR_INVALID_ARG;
+    if (cu_q && N == 0 && (T > 0 || Tk > 0)) return KDA_ERR_INVALID_ARG;       // tokens of no sequence
     if (!(scale > 0.f) || scale > 3.0e38f) return KDA_ERR_INVALID_ARG;
     if (!workspace || !al(workspace, 16) || need == 0 || workspace_bytes < need) return KDA_ERR_INVALID_ARG;
     if (dtype != KDA_BF16 || dk != kHeadDim || dv != kHeadDim || (dr != 0 && dr != kSharedDim)) return KDA_ERR_UNSUPPORTED;
@@ -376,6 +383,11 @@ kda_status_t check_latent(const void *q, const void *k, const void *v, const voi
     a->B = B; a->T = T; a->Tk = Tk; a->H = H; a->N = N; a->R = dr; a->scale = scale;
     a->status = (int32_t *)workspace;
     return KDA_OK;
+}
+
+cudaError_t launch_latent_check(const LatentArgs &a, cudaStream_t stream)
+{
+    return launch_after(latent_check_kernel, 1, 256, 0, stream, a);
 }
 
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream)
@@ -421,8 +433,8 @@ kda_status_t kda_latent_fwd(const void *q, const void *k, const void *v, const v
     if (s != KDA_OK) return s;
     a.causal = causal != 0;
     cudaStream_t st = (cudaStream_t)stream;
-    if ((long long)B * T == 0 || N == 0) return cudaMemsetAsync(workspace, 0, kStatusBytes, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
-    return launch_latent_fwd(a, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    const cudaError_t e = (long long)B * T == 0 || N == 0 ? launch_latent_check(a, st) : launch_latent_fwd(a, st);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 }  // extern "C"

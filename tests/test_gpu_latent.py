@@ -191,6 +191,21 @@ def test_expanded_bad_offsets_are_reported_and_skipped():
     check_forward(q, k, v, r, lens, lens, True, out, lse)
 
 
+def test_expanded_offsets_are_checked_where_there_is_no_query():
+    for keys, offs_q, offs_k, status in (
+            (5, [0, 0], [0, 5], kda.KDA_OK), (5, [0, 0], [0, 3], kda.KDA_ERR_INVALID_ARG), (5, [0, 0, 0], [0, 6, 5], kda.KDA_ERR_INVALID_ARG),
+            (5, [0, 1], [0, 5], kda.KDA_ERR_INVALID_ARG), (0, [0, 0], [0, 0], kda.KDA_OK), (0, [0, 0], [0, 1], kda.KDA_ERR_INVALID_ARG),
+            (0, [2, 0], [0, 0], kda.KDA_ERR_INVALID_ARG)):
+        q, k, v, r, dout = expanded([0], [keys], 2, 64)
+        cu = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in (offs_q, offs_k)]
+        ws = torch.full((256,), 255, dtype=torch.uint8, device=DEV)
+        out, lse = kda.latent_fwd(q, k, v, r, *cu, workspace=ws)
+        assert kda.workspace_status(ws) == status, (offs_q, offs_k)
+        ws = torch.full((kda.latent_bwd_workspace_size(1, 0, keys, 2, len(offs_q) - 1),), 255, dtype=torch.uint8, device=DEV)
+        kda.latent_bwd(q, k, v, r, out, lse, dout, *cu, workspace=ws)
+        assert kda.workspace_status(ws) == status, (offs_q, offs_k)
+
+
 def test_expanded_empty_sizes():
     q, k, v, r, dout = expanded([4], [0], 2, 64)
     out, lse = kda.latent_fwd(q, k, v, r, cu_of([4]), cu_of([0]))

@@ -144,6 +144,12 @@ def test_latent_host_checks(lib, call):
             assert call(lib, **kw) == bad, kw
 
 
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+def test_latent_tokens_of_no_sequence_are_refused(lib, call):
+    for kw in (dict(T=8, Tk=8), dict(T=8, Tk=0), dict(T=0, Tk=8)):
+        assert call(lib, cu=A, cuk=A, N=0, **kw) == kda.KDA_ERR_INVALID_ARG, kw
+
+
 def _dec(lib, **kw):
     a = dict(q=A, cache=A, table=A, lens=A, out=A, lse=A, N=2, Tq=1, H=4, dc=512, dr=64, page=64, pages=8, maxp=4, scale=0.1,
              dtype=1, ws=A, wsb=1 << 30)
