@@ -64,7 +64,9 @@ def _p(t):
 def _rows(name, t, B, L, H, D):
     """Token and head strides of a [B, L, H, D] view whose batch rows follow one another."""
     sb, st, sh, sc = t.stride()
-    if sc != 1 or (B > 1 and sb != L * st):
+    if L == 1:
+        st = sb                           # batch rows of one token: the stride between them is the tokens'
+    if sc != 1 or (B > 1 and L > 1 and sb != L * st):
         raise ValueError("%s: channels must be contiguous and batch rows follow one another" % name)
     # a stride along an axis of one element is never used; the library wants a plausible one
     return (st if B * L > 1 else max(st, 8) // 8 * 8), (sh if H > 1 else D)
@@ -86,7 +88,9 @@ def _expanded(q, k, v, k_shared, cu_q, cu_k):
     if k_shared is not None:
         _check("k_shared", k_shared, _BF16, dev, (B, Tk, dr), dense=False)
         sb, rs, sc = k_shared.stride()
-        if sc != 1 or (B > 1 and sb != Tk * rs):
+        if Tk == 1:
+            rs = sb
+        if sc != 1 or (B > 1 and Tk > 1 and sb != Tk * rs):
             raise ValueError("k_shared: channels must be contiguous and batch rows follow one another")
         rs = rs if B * Tk > 1 else dr
     N = B

@@ -127,6 +127,21 @@ def test_expanded_batch_rows_without_offsets(H, T, Tk):
         assert torch.equal(g[key].reshape(p[key].shape), p[key]), key
 
 
+def test_expanded_batch_rows_of_one_key_or_none():
+    """Views whose batch rows hold one key each (``t[:, :1]``), and batch rows without keys."""
+    B, H = 3, 2
+    q, kv, wide, dout = (torch.randn(*s, device=DEV).to(B16) for s in ((B, 4, H, 192), (B, 5, H, 256), (B, 5, 576), (B, 4, H, 128)))
+    k, v, r = kv[:, :1, :, :128], kv[:, :1, :, 128:], wide[:, :1, 512:]
+    for causal in (True, False):
+        out, lse = kda.latent_fwd(q, k, v, r, causal=causal)
+        want = kda.latent_fwd(q, k.contiguous(), v.contiguous(), r.contiguous(), causal=causal)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        g, w = (kda.latent_bwd(q, *a, out, lse, dout, causal=causal) for a in ((k, v, r), (k.contiguous(), v.contiguous(), r.contiguous())))
+        assert all(torch.equal(g[x], w[x]) for x in g)
+    out, lse = kda.latent_fwd(q, kv[:, :0, :, :128], kv[:, :0, :, 128:], wide[:, :0, 512:])
+    assert torch.all(out == 0) and torch.all(lse == -float("inf"))
+
+
 def test_expanded_head_major_and_dense_layouts_agree():
     lens = [130, 77]
     q, k, v, r, dout = expanded(lens, lens, 4, 64, seed=9)

@@ -207,6 +207,19 @@ def test_norm_host_checks(lib):
     assert kda.rms_norm_bwd_workspace_size(4, 100) == 0 and kda.rms_norm_bwd_workspace_size(4, 256) == 4 * 256 * 4
 
 
+def test_strides_of_batch_rows():
+    """Token and head strides of views, rows of one token among them (whose token stride is the batch's)."""
+    from kimi_delta_attention_25_b200 import latent
+    t = torch.zeros(3, 5, 2, 256)
+    rows = lambda x: latent._rows("k", x, *x.shape)  # noqa: E731
+    assert rows(t) == (512, 256) and rows(t[..., :128]) == (512, 256)
+    assert rows(t[:, :1]) == (2560, 256) and rows(t[:, 2:3, :, 128:]) == (2560, 256) and rows(t[:1, :1])[1] == 256
+    assert rows(t[:, :0])[0] > 0
+    for bad in (t[:, :2], t[:, 1:4], t.transpose(0, 1), t[..., ::2]):
+        with pytest.raises(ValueError):
+            rows(bad)
+
+
 def test_binding_refuses_cpu_tensors_types_and_shapes():
     b = torch.bfloat16
     q, k = torch.zeros(1, 4, 2, 192, dtype=b), torch.zeros(1, 4, 2, 128, dtype=b)
