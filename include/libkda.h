@@ -483,6 +483,7 @@ kda_status_t kda_latent_append(const void *c, const void *k_shared, const long l
  *   alias x or residual when the other does not need them. Sums are fp32. 16-byte aligned pointers.
  * kda_rms_norm_e4m3 writes y in 8 bits (e4m3) instead, with one fp32 scale per 128 channels (D a
  * multiple of 128): scale [rows, D / 128] = max |y| / 448, y = q * scale. A group of zeros gets scale 0.
+ * This y overlaps none of x, residual and h (KDA_ERR_INVALID_ARG).
  * A group that holds a NaN or an infinity has a scale that is not finite. */
 kda_status_t kda_rms_norm(const void *x, const void *residual, const float *weight, void *y, void *h,
                           long long rows, int D, float eps, kda_dtype_t dtype, void *stream);

@@ -424,6 +424,12 @@ kda_status_t run_norm(const void *x, const void *residual, const float *weight, 
     if (!x || !weight || !y || (q8 && !scale) || (residual && !h)) return KDA_ERR_INVALID_ARG;
     if (!al(x, 16) || !al(residual, 16) || !al(weight, 16) || !al(y, 16) || !al(h, 16) || !al(scale, 4))
         return KDA_ERR_INVALID_ARG;
+    if (q8) {
+        // rows of y have other places than those of x: another block would write over what one has yet to read
+        const uintptr_t y0 = (uintptr_t)y, y1 = y0 + (size_t)rows * D, wide = (size_t)rows * D * (dtype == KDA_BF16 ? 2 : 4);
+        for (const void *t : {x, residual, (const void *)h})
+            if (t && y0 < (uintptr_t)t + wide && (uintptr_t)t < y1) return KDA_ERR_INVALID_ARG;
+    }
     NormParams p;
     p.x = x; p.res = residual; p.w = weight; p.y = y; p.h = h; p.scale = scale; p.eps = eps; p.inv_d = 1.f / (float)D;
     p.rows = rows; p.D = D;

@@ -207,6 +207,15 @@ def test_norm_host_checks(lib):
     assert kda.rms_norm_bwd_workspace_size(4, 100) == 0 and kda.rms_norm_bwd_workspace_size(4, 256) == 4 * 256 * 4
 
 
+def test_norm_e4m3_refuses_an_output_over_its_inputs(lib):
+    """The 8-bit rows lie elsewhere than the rows they come from, so writing them in place would race."""
+    P, size = ctypes.c_void_p, 4 * 256 * 2
+    far = A + 64 * size
+    for x, res, h, y in ((A, None, None, A), (A, None, None, A + size - 16), (A + 512, None, None, A), (far, A, far + size, A + 256),
+                         (far, far + size, A, A)):
+        assert lib.kda_rms_norm_e4m3(P(x), P(res), P(A), P(y), P(far + 8 * size), P(h), 4, 256, 1e-5, 1, None) == kda.KDA_ERR_INVALID_ARG
+
+
 def test_strides_of_batch_rows():
     """Token and head strides of views, rows of one token among them (whose token stride is the batch's)."""
     from kimi_delta_attention_25_b200 import latent
