@@ -411,7 +411,7 @@ kda_status_t kda_chunk_fwd_noalloc_status(void *stream, int32_t *status);
  * queries that the mask hides it from, of the same 128 (0 times it is NaN there).
  *   workspace  kda_latent_fwd_workspace_size(...) bytes; its status word is cleared by the call.
  * Strides are positive multiples of 8; pointers 16-byte aligned (lse, offsets: 4). At most 65535 heads
- * and 65535 sequences. */
+ * and 65535 sequences, and H * (B T / 64 + B Tk / 64 + 2 N + 1) below 2^31 (else KDA_ERR_UNSUPPORTED). */
 size_t kda_latent_fwd_workspace_size(int B, int T, int Tk, int H, int N, int dr);
 kda_status_t kda_latent_fwd(const void *q, const void *k, const void *v, const void *k_shared,
                             const int32_t *cu_seqlens, const int32_t *cu_seqlens_k,

@@ -811,7 +811,6 @@ cudaError_t launch_latent_bwd(const LatentArgs &a, const LatentBwdArgs &b, cudaS
     const long long tokens = (long long)a.B * a.T, keys = (long long)a.B * a.Tk;
     const long long q_slots = tokens > 0 ? tokens / TL + a.N : 0, k_slots = keys > 0 ? keys / TL + a.N : 0;
     const long long stat_blocks = (tokens + 8 * kStatTokens - 1) / (8 * kStatTokens) * a.H;
-    if ((q_slots + k_slots) * a.H > 0x7fffffffLL || stat_blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int W = kHeadDim + a.R;
     BwdMaps m = {};                                               // an empty side's tiles are never copied
     if (tokens > 0 && (!bf16_heads_map(&m.q, a.q, W, a.H, tokens, W, (long long)a.H * W, 64, TL) ||
@@ -866,6 +865,9 @@ kda_status_t kda_latent_bwd(const void *q, const void *k, const void *v, const v
     if ((long long)B * T > 0 && (!dout || !dq)) return KDA_ERR_INVALID_ARG;
     if ((long long)B * Tk > 0 && (!dk_out || !dv_out || (dr && !dk_shared))) return KDA_ERR_INVALID_ARG;
     if (!al(dout, 16) || !al(dq, 16) || !al(dk_out, 16) || !al(dv_out, 16) || !al(dk_shared, 16)) return KDA_ERR_INVALID_ARG;
+    const long long tokens = (long long)B * T, keys = (long long)B * Tk;
+    if ((tokens / TL + keys / TL + 2LL * N) * H > 0x7fffffffLL || (tokens / (8 * kStatTokens) + 1) * H > 0x7fffffffLL)
+        return KDA_ERR_UNSUPPORTED;                               // blocks of a launch
     a.causal = causal != 0;
     LatentBwdArgs b;
     b.dout = (const __nv_bfloat16 *)dout;

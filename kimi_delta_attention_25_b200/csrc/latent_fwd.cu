@@ -393,7 +393,6 @@ cudaError_t launch_latent_check(const LatentArgs &a, cudaStream_t stream)
 cudaError_t launch_latent_fwd(const LatentArgs &a, cudaStream_t stream)
 {
     const long long tokens = (long long)a.B * a.T, keys = (long long)a.B * a.Tk, slots = tokens / (2 * QT) + a.N;
-    if (slots * a.H > 0x7fffffffLL) return cudaErrorInvalidValue;
     const int W = kHeadDim + a.R;
     CUtensorMap tq = {}, tk = {}, tv = {}, tr = {};
     if (!bf16_heads_map(&tq, a.q, W, a.H, tokens, W, (long long)a.H * W, 64, QT)) return cudaErrorNotSupported;
@@ -433,6 +432,7 @@ kda_status_t kda_latent_fwd(const void *q, const void *k, const void *v, const v
     if (s != KDA_OK) return s;
     a.causal = causal != 0;
     cudaStream_t st = (cudaStream_t)stream;
+    if (((long long)B * T / (2 * QT) + N) * H > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;      // blocks of a launch
     const cudaError_t e = (long long)B * T == 0 || N == 0 ? launch_latent_check(a, st) : launch_latent_fwd(a, st);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

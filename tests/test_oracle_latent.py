@@ -150,6 +150,12 @@ def test_latent_tokens_of_no_sequence_are_refused(lib, call):
         assert call(lib, cu=A, cuk=A, N=0, **kw) == kda.KDA_ERR_INVALID_ARG, kw
 
 
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+def test_latent_more_blocks_than_a_launch_takes_are_unsupported(lib, call):
+    for kw in (dict(T=1 << 30, H=1024), dict(T=1 << 24, H=65535), dict(T=64, Tk=64, H=65535, N=65535, cu=A, cuk=A)):
+        assert call(lib, wsb=1 << 50, **kw) == kda.KDA_ERR_UNSUPPORTED, kw
+
+
 def _dec(lib, **kw):
     a = dict(q=A, cache=A, table=A, lens=A, out=A, lse=A, N=2, Tq=1, H=4, dc=512, dr=64, page=64, pages=8, maxp=4, scale=0.1,
              dtype=1, ws=A, wsb=1 << 30)
