@@ -248,6 +248,63 @@ def test_expanded_backward_over_many_query_tiles(R):
         check_backward(q, k, v, r, dout, lens_q, lens_k, causal, g)
 
 
+@pytest.mark.parametrize("N", [40, 60, 70, 380, 390, 1100])
+def test_expanded_many_sequences(N):
+    """More sequences than a warp's first look at the offsets, and so many blocks that they are no longer
+    ranked; empty sequences and ones without queries or without keys among them."""
+    rng = np.random.default_rng(N)
+    lens_q = np.minimum(rng.integers(0, 3, N) * rng.integers(0, 6, N), 9)
+    lens_k = np.where(rng.random(N) < 0.1, 0, lens_q + rng.integers(0, 4, N))
+    if N == 40:
+        lens_q, lens_k = lens_q * 30, lens_k * 31
+    elif N == 380:
+        lens_q = np.minimum(lens_q, 3)
+    lens_q, lens_k = lens_q.tolist(), lens_k.tolist()
+    q, k, v, r, dout = expanded(lens_q, lens_k, 2, 64, seed=N)
+    cu = (cu_of(lens_q), cu_of(lens_k))
+    out, lse, ws = kda.latent_fwd(q, k, v, r, *cu, return_workspace=True)
+    assert kda.workspace_status(ws) == kda.KDA_OK
+    ro = check_forward(q, k, v, r, lens_q, lens_k, True, out, lse)
+    out = torch.tensor(ro, dtype=torch.float32, device=DEV).to(B16)[None]
+    g, ws = kda.latent_bwd(q, k, v, r, out, lse, dout, *cu, return_workspace=True)
+    assert kda.workspace_status(ws) == kda.KDA_OK
+    check_backward(q, k, v, r, dout, lens_q, lens_k, True, g)
+
+
+@pytest.mark.parametrize("R", [64, 0])
+@pytest.mark.parametrize("lens_q,lens_k", [([70], [900]), ([300, 130], [700, 800])])
+def test_expanded_growing_scores(lens_q, lens_k, R):
+    """Scores that rise by some 13 (19 in the log2 domain) over each tile of 128 keys, so that every row's maximum moves
+    in every tile by more than the 2^15 that the forward pass lets pass."""
+    H, W = 2, 128 + R
+    q, k, v, r, dout = expanded(lens_q, lens_k, H, R, seed=17)
+    g = torch.Generator().manual_seed(18)
+    sign = torch.randn(128, generator=g).sign()
+    ramp = torch.cat([torch.arange(n) / 128.0 for n in lens_k])[None, :, None, None]
+    k = (ramp * sign + 0.05 * torch.randn(1, sum(lens_k), H, 128, generator=g)).to(B16).to(DEV)
+    q = torch.cat([(sign + 0.05 * torch.randn(1, sum(lens_q), H, 128, generator=g)), 0.2 * torch.randn(1, sum(lens_q), H, R, generator=g)], -1).to(B16).to(DEV)
+    cu = (cu_of(lens_q), cu_of(lens_k))
+    for causal in (True, False):
+        out, lse = kda.latent_fwd(q, k, v, r, *cu, causal=causal, scale=0.1)
+        ro = check_forward(q, k, v, r, lens_q, lens_k, causal, out, lse, 0.1)
+        grads = kda.latent_bwd(q, k, v, r, torch.tensor(ro, dtype=torch.float32, device=DEV).to(B16)[None], lse, dout, *cu, causal=causal, scale=0.1)
+        check_backward(q, k, v, r, dout, lens_q, lens_k, causal, grads, 0.1)
+
+
+@pytest.mark.parametrize("lens_q,lens_k", [([130], [6000]), ([64], [131072]), ([2100], [2100])])
+def test_expanded_long(lens_q, lens_k):
+    """A few queries behind a long history, and a prompt of several blocks."""
+    q, k, v, r, dout = expanded(lens_q, lens_k, 1, 64, seed=lens_k[0])
+    cu = (cu_of(lens_q), cu_of(lens_k))
+    out, lse, ws = kda.latent_fwd(q, k, v, r, *cu, return_workspace=True)
+    assert kda.workspace_status(ws) == kda.KDA_OK
+    ro = check_forward(q, k, v, r, lens_q, lens_k, True, out, lse)
+    out = torch.tensor(ro, dtype=torch.float32, device=DEV).to(B16)[None]
+    g, ws = kda.latent_bwd(q, k, v, r, out, lse, dout, *cu, return_workspace=True)
+    assert kda.workspace_status(ws) == kda.KDA_OK
+    check_backward(q, k, v, r, dout, lens_q, lens_k, True, g)
+
+
 def test_expanded_gradients_of_short_rows():
     """Rows that see one key have no gradient through the softmax (exactly), and those that see a few keep their
     accuracy although ``out`` was rounded: over all rows two roundings to bf16, each at most 2^-8 of a value and of
@@ -383,6 +440,19 @@ def test_absorbed_long_sequence_split_over_the_gpu():
     out, lse = kda.latent_decode_step(q, cache, table, lens)
     assert all(torch.equal(out[0, 0, h], out[0, 0, 0]) for h in range(16))
     check_decode(q[:, :, :1], cache, table, lens, out[:, :, :1], lse[:, :, :1], 192 ** -0.5)
+
+
+@pytest.mark.parametrize("H", [8, 48, 128])
+def test_absorbed_short_sequences_beside_a_long_one(H):
+    """As many sequences as shares of the GPU, nearly, and one of them cut into many parts: the join goes by share and
+    takes a block to a row."""
+    lens = [(i * 37) % 160 for i in range(60)] + [20000] + [(i * 53) % 160 for i in range(45)]
+    a = paged(lens, H, 64, 1, 64, seed=H)
+    out, lse, ws = kda.latent_decode_step(*a, return_workspace=True)
+    assert kda.workspace_status(ws) == kda.KDA_OK
+    check_decode(*a, out, lse, 192 ** -0.5)
+    again = kda.latent_decode_step(*a)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
 def test_absorbed_peaked_and_growing_scores():
@@ -538,6 +608,12 @@ def test_rms_norm_e4m3(rows, D, dtype):
         assert np.mean(exact != got) <= 1e-3            # only ties within the fp32 error may fall the other way
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,D", [(2051, 512), (700, 4096), (300, 8320)])
+def test_rms_norm_e4m3_of_many_rows(rows, D, dtype):
+    test_rms_norm_e4m3(rows, D, dtype)
+
+
 def test_rms_norm_e4m3_non_finite_groups_say_so():
     x = torch.randn(3, 384, device=DEV)
     x[1, 130] = float("nan")
@@ -584,6 +660,27 @@ def test_append(T, R, page):
     for t, s in enumerate(slots.tolist()):
         if 0 <= s < pages * page:
             assert torch.equal(plain.view(-1, 512 + R)[s], x[t])
+
+
+@pytest.mark.parametrize("R", [64, 0])
+@pytest.mark.parametrize("T", [1, 2, 9])
+def test_append_of_the_first_token(T, R):
+    """Every token has a row, the first and only one too; with the norm and as it is."""
+    g = torch.Generator().manual_seed(T + R)
+    x = torch.randn(T, 640, generator=g).to(B16).to(DEV)
+    w = (1 + 0.1 * torch.randn(512, generator=g)).to(DEV)
+    before = torch.randn(3, 16, 512 + R, generator=g).to(B16).to(DEV)
+    slots = torch.randperm(48, generator=g)[:T]
+    c, r = x[:, :512], x[:, 512:512 + R] if R else None
+    cache = kda.latent_append(c, r, before.clone(), slots.to(DEV), weight=w)
+    want = f64(before).reshape(48, -1)
+    ref, got = O.rms_norm(f64(c), f64(w), 1e-5), f64(cache).reshape(48, -1)
+    assert np.all(np.abs(got[slots, :512] - ref) <= (HALF + 300 * 2.0 ** -24) * np.abs(ref) + 1e-30)
+    want[slots, :512] = got[slots, :512]
+    want[slots, 512:] = f64(x)[:, 512:512 + R]
+    assert np.array_equal(got, want)                     # the shared part as it is, every other row as it was
+    plain = kda.latent_append(c, r, before.clone(), slots.to(DEV))
+    assert torch.equal(plain.view(48, -1)[slots], x[:, :512 + R])
 
 
 # ------------------------------------------------------------------------------------ used together
