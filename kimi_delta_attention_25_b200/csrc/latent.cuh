@@ -72,12 +72,14 @@ __device__ __forceinline__ bool latent_slot(const int32_t *cu, const LatentArgs 
 }
 
 // The query tile (of `tile` rows) whose row of key tiles is the rank-th longest, of packed sequences, where the slots'
-// order says nothing about it: with few blocks to an SM the last ones should be the shortest (9 sequences of some 300
-// queries behind histories, 16 heads: 88 us in slot order, 75 so). Every block counts for itself, so only up to
-// kRankedSlots slots, behind which there are blocks enough to even it out. All of the block's threads; `scratch` is
-// shared memory for 2 slots + 1 integers, which the caller may use again when this returns (bulk copies: behind a
-// proxy fence).
-constexpr int kRankedSlots = 384;
+// order says nothing about it: with few blocks to an SM the last ones should be the shortest. Every block counts for
+// itself, a time that grows with the square of the slots, so only up to kRankedSlots slots. Ranked and in slot order, 4 and
+// 16 heads: 60 slots behind histories of up to 1500 keys 31 and 44 us, 109 and 115 us (9 sequences of some 300 queries
+// behind histories, 16 heads: 75 and 88), prompts of up to 50 tokens 17 and 16 us, 55 and 50 us; 122 slots 63 and 69,
+// 242 and 231 behind histories, 34 and 29, 111 and 97 for prompts; 375 slots 257 and 179, 999 and 658, and 167 and 73, 665 and
+// 291 for prompts. All of the block's threads; `scratch` is shared memory for 2 slots + 1 integers, which the caller may use
+// again when this returns (bulk copies: behind a proxy fence).
+constexpr int kRankedSlots = 64;
 __device__ __forceinline__ bool latent_ranked(const LatentArgs &a, int tile, int slots, int rank, int *scratch, LatentSpan *s,
                                               long long *row)
 {
