@@ -426,7 +426,9 @@ kda_status_t kda_latent_fwd(const void *q, const void *k, const void *v, const v
  * Written, dense and bf16 (summed in fp32, rounded once): dq [B, T, H, dk + dr], dk_out and dv_out
  * [B, Tk, H, 128], dk_shared [B, Tk, dr] (the sum over the heads; NULL when dr = 0). Results do not
  * depend on timing: no atomic sums. A query that sees one key has no gradient through its score
- * (exactly 0). Workspace: kda_latent_bwd_workspace_size(...) bytes. Keys that no
+ * (exactly 0). P and dS are rounded to bf16 as operands; for queries that see more than 16 keys dout . out
+ * is taken from the rounded out, so a score's gradient P (dP - dout . out) is off by up to 2^-8 P |dout| . |out|,
+ * which is most of it where one key has nearly all of a query's probability. Workspace: kda_latent_bwd_workspace_size(...) bytes. Keys that no
  * query sees get zero gradients. */
 size_t kda_latent_bwd_workspace_size(int B, int T, int Tk, int H, int N, int dr);
 kda_status_t kda_latent_bwd(const void *q, const void *k, const void *v, const void *k_shared,

@@ -10,7 +10,7 @@
 // The tensor cores bound it: per 128 x 128 tile and head 804 + 536 + 792 cycles for dq and 804 + 3 x 536 + 280 for dk and
 // dv, 4820 in all, where a single pass without the recomputation would take 3460. Measured: 2690 for dq and 3650 for dk
 // and dv, where each tile's chain of scores, exponentials and P's product is the longer; 8192 tokens x 16 heads, causal,
-// 0.96 ms alone, 1.12 under the power cap.
+// 0.96 to 0.99 ms alone, 1.10 to 1.12 under the power cap.
 // dS and P pass through tensor memory in bf16 as A operands; sums, lse and D are fp32.
 #include "latent.cuh"
 #include "sm100.cuh"
@@ -41,9 +41,11 @@ __device__ __forceinline__ float dot8(const uint4 &x, const uint4 &y)
 // lse in the log2 domain and D_i = do_i . o_i as [H][tokens] (the dk and dv blocks read them along the
 // tokens): one warp per head and eight tokens, half a warp to a row, all its rows on their way at once (two tokens to a
 // warp took twice the time).
-// `out` has been rounded to bf16, which moves D by up to 2^-8 of |do| . |o|. Beside the rounding of dS itself that
-// matters where a row sees few keys (dS is then a difference of nearly equal values, and o as large as v): rows
-// that see at most kShortRow keys get D = sum_j P_ij dP_ij instead, from the same sums in fp32.
+// `out` has been rounded to bf16, which moves D by up to 2^-8 of |do| . |o|, and dS = P (dP - D) by P times that. Beside
+// the rounding of dS itself that matters where one key has most of a row's probability (dS is then a difference of nearly
+// equal values, and o as large as v). Rows that see at most kShortRow keys, where that is the rule, get D = sum_j P_ij dP_ij
+// instead, from the same sums in fp32. A longer row that one key takes (P near 1) keeps D from `out`: recomputing D for all
+// rows would take scores and dP once more, a quarter of the products there are.
 constexpr int kShortRow = 16, kStatTokens = 8;
 static_assert(8 * kStatTokens <= 64, "a block's tokens, a bit each");
 __global__ void __launch_bounds__(256) latent_stat_kernel(LatentArgs a, const __nv_bfloat16 *__restrict__ dout, float *__restrict__ stat,

@@ -13,7 +13,7 @@
 //  - The products are limited by what they read from shared memory (A 128 rows x 16 = 4 KB an instruction at
 //    128 bytes a cycle), which the copies' writes share: S^T with M = 64 reads 3 KB where S = Q C^T with
 //    M = 128 (rows behind the queries unused) reads 6 KB and took 52 cycles an instruction (256 sequences x 32
-//    heads, 1.5 GB: 392 us, then 342 with nothing else changed; 256 to 282 now, 5.4 to 5.9 TB/s).
+//    heads, 1.5 GB: 392 us, then 342 with nothing else changed; 253 to 268 now, 5.7 to 6.0 TB/s).
 //  - A thread of the softmax has one cache row and 16 of the query rows. It goes on with the running maxima
 //    it has and only checks, in the same barrier that the tile needs anyway, whether a score passed one of
 //    them by more than 2^8 (P stays below 2^8, l is fp32): maxima across threads, and the rescaling of O^T in

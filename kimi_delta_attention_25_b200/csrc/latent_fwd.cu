@@ -21,8 +21,8 @@
 //    and warp-uniform with one issuing thread, so that descriptors stay in uniform registers.
 //  - Keys wait in a ring of four units (128 rows x 64 channels, the shared part a tile's third), freed one by one,
 //    values in two whole tiles: with one of either the products waited for copies.
-// Blocks run from the longest row of tiles to the shortest. 8192 tokens x 32 heads, causal: 540 us (1.27 PFLOP/s),
-// 619 in a row of calls under the power cap; the tensor pipe is active for 57 % of the cycles. P's rounding to bf16
+// Blocks run from the longest row of tiles to the shortest. 8192 tokens x 32 heads, causal: 532 to 541 us (1.27 PFLOP/s),
+// 620 to 628 in a row of calls under the power cap; the tensor pipe is active for 57 % of the cycles. P's rounding to bf16
 // is the operand type's; sums and statistics are fp32.
 #include "latent.cuh"
 #include "sm100.cuh"

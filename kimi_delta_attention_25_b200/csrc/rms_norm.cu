@@ -182,8 +182,8 @@ __device__ __forceinline__ void bulk_row(void *dst, const void *src, uint32_t by
 // TPR threads hold one row, and the block walks its rows with the weight gradient's sum in registers;
 // a second kernel adds the blocks' sums in a fixed order, so results do not depend on timing. Up to 1024 vectors
 // a row (one a thread) the rows come through shared memory, kRowsAhead of them by bulk copies of one thread, which
-// keeps 190 KB an SM on their way without a register (8192 x 4096 bf16: rows loaded into registers one ahead took
-// 55 us, this 45); wider rows are loaded as they are needed.
+// keeps 190 KB an SM on their way without a register (8192 x 4096 bf16, both kernels: rows loaded into registers one
+// ahead took 67 us, this 50 to 52); wider rows are loaded as they are needed.
 constexpr int kRowsAhead = 4;
 template <typename T, int TPR, int VPT, bool DH>
 __global__ void __launch_bounds__(TPR) rms_norm_bwd_kernel(NormBwdParams p)
